@@ -347,6 +347,114 @@ ROD_API int rod_swska_cache_fill_fp8(const void* k, const void* v, void* k_cache
                                      int H, int T, int dk, int dv, int window, float k_scale,
                                      float v_scale, void* stream);
 
+/* ---- SW-SKA with first tokens that stay visible ------------------------------------------- */
+/*
+ * SW-SKA in which the first `sinks` tokens of a sequence stay visible to every later query (the
+ * sliding window of CodeFuse's SKA and SALA blog §2.1, plus the tokens at the start that such a
+ * window would drop): query t sees the keys j <= t with j > t - window or j < sinks,
+ *   o[h,t] = sum_j p_tj v[h,j],  p_tj = softmax_j(scale * q[h,t] . k[j]),
+ *   lse[h,t] = log sum_j exp(scale * q[h,t] . k[j])   (natural log).
+ * rod_swska_sink_prefill: q [B,H,T,dk], k [B,T,dk] (shared by the heads), v [B,H,T,dv], o [B,H,T,dv]:
+ * dtype; lse [B,H,T] fp32, 4-byte aligned. window >= 1, 0 <= sinks <= ROD_MAX_SINKS, scale as for
+ * rod_swska_prefill; sinks = 0 is rod_swska_prefill_lse.
+ * rod_swska_sink_backward: the gradients for the loss gradient dO of o, from the forward's o and lse
+ * with the same inputs (as rod_swska_backward_lse):
+ *   D_t = dO_t . o_t;  dS_tj = p_tj (dO_t . v_j - D_t);  dq_t = scale sum_j dS_tj k_j;
+ *   dk_j = scale sum_h sum_t dS_tj q_t;  dv_j = sum_t p_tj dO_t (per head);
+ * outputs dq, dk, dv in the layouts and dtype of q, k, v; workspace of
+ * rod_swska_sink_backward_workspace_size bytes (its content on entry is irrelevant). Every sum is
+ * taken in a fixed order: the results do not depend on timing.
+ * Two routes, chosen by dtype and shape: ROD_BF16 with dk = dv = 128 and T >= 128 runs on the tensor
+ * cores (bf16 probabilities and dS, fp32 accumulators), every other case on CUDA cores with fp32
+ * FMAs.
+ * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE (window < 1, sinks or dims unsupported, H > 64), ROD_ERR_ALIGN,
+ * ROD_ERR_DTYPE, ROD_ERR_WORKSPACE, ROD_ERR_CUDA. T = 0 or B*H = 0 is a no-op.
+ */
+#define ROD_MAX_SINKS 128
+ROD_API int rod_swska_sink_prefill(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                                   int H, int T, int dk, int dv, int window, int sinks, float scale,
+                                   int dtype, void* stream);
+ROD_API size_t rod_swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int window,
+                                                      int sinks);
+ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v, const void* o,
+                                    const float* lse, const void* dO, void* dq, void* dk, void* dv, int B,
+                                    int H, int T, int dk_dim, int dv_dim, int window, int sinks,
+                                    float scale, int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- SW-SKA: new tokens over a paged cache ------------------------------------------------- */
+/*
+ * Attention of a ragged batch of new tokens -- one, a few or a long chunk per sequence -- over a cache
+ * kept in pages (SALA blog §3.3: chunked prefill over a paged KV cache; its decode step is the
+ * case of one token each). Unlike rod_swska_decode_paged, whose pages form a ring of W slots, the
+ * pages here hold absolute positions: position p of sequence n sits in row p mod page_size of
+ * physical page block_table[n, p / page_size].
+ *   q [M,H,dk], k_new [M,dk], v_new [M,H,dv], o [M,H,dv]: dtype. Rows cu_seqlens[n] ..
+ *   cu_seqlens[n+1] - 1 are sequence n's new tokens, at positions ctx[n], ctx[n] + 1, ...; rows past
+ *   cu_seqlens[N] belong to no sequence (a padded batch): their o keeps what it holds.
+ *   k_pool [P][page_size][dk], v_pool [P][H][page_size][dv]: dtype (the layout of
+ *   rod_swska_decode_paged);
+ *   block_table [N][max_pages] int32: physical pages; an entry outside [0, P) is no page;
+ *   slot_map [M] int32: row i of k_new / v_new is first written to slot slot_map[i] (physical page *
+ *   page_size + row in the page); a slot outside [0, P * page_size) is not written;
+ *   cu_seqlens [N+1] int32, not decreasing, cu_seqlens[0] >= 0; ctx [N] int64: tokens cached before.
+ * k_new, v_new and slot_map may be NULL together: nothing is written, the cache has the tokens.
+ * Then query i of sequence n, at position p = ctx[n] + i, attends over the keys j <= p with
+ * j > p - window or j < sinks, read from the cache. Keys of pages that the table does not have are
+ * left out (as pages behind the window are, once given back); a row that sees no key is 0. Memory
+ * of a page past its sequence's last token may hold anything. A sequence with ctx[n] < 0 or a
+ * position past 2^31 - 1 gets NaN rows. A sequence may have no new token.
+ *   max_len: at most this many new tokens per sequence (a bound that picks the kernels; 0: M); of a
+ *   longer sequence only the first max_len rows are computed.
+ * workspace: rod_swska_extend_paged_workspace_size bytes, content irrelevant on entry. Two calls that
+ * may overlap (two streams, two graphs) need a workspace each.
+ * page_size: a positive multiple of 8; P * page_size and max_pages * page_size at most 2^31 - 1;
+ * 1 <= H <= 64; 0 <= sinks <= ROD_MAX_SINKS; N <= ROD_MAX_EXTEND_SEQS.
+ * Routes: ROD_BF16 with dk = dv = 128 runs on the tensor cores, every other case on CUDA cores with
+ * fp32 FMAs. The result does not depend on timing.
+ * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE, ROD_ERR_ALIGN (ctx: 8 bytes; int32 arrays: 4), ROD_ERR_DTYPE,
+ * ROD_ERR_WORKSPACE, ROD_ERR_CUDA. M = 0 or N = 0 is a no-op.
+ */
+#define ROD_MAX_EXTEND_SEQS 16384
+ROD_API size_t rod_swska_extend_paged_workspace_size(int M, int N, int H, int dk, int dv, int max_len,
+                                                     int dtype);
+ROD_API int rod_swska_extend_paged(const void* q, const void* k_new, const void* v_new, void* k_pool,
+                                   void* v_pool, const int32_t* block_table, const int32_t* slot_map,
+                                   const int32_t* cu_seqlens, const int64_t* ctx, void* o, int M, int N,
+                                   int H, int dk, int dv, int P, int page_size, int max_pages, int window,
+                                   int sinks, int max_len, float scale, int dtype, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* ---- SW-SKA: block tables and slot map of a paged cache ------------------------------------ */
+/*
+ * One step of the bookkeeping of rod_swska_extend_paged's cache, on the device (SALA blog §3.3: small
+ * blocks, allocated on demand and evicted by window). Sequence n has ctx[n] cached tokens and wants
+ * room for n_new[n] more (0: none this step; negative: the sequence is finished).
+ *   block_table [N][max_pages] int32, in/out: entries outside [0, P) mean "no page" (-1 is written);
+ *   first [N] int32, in/out, 0 for a fresh sequence: logical pages in [ceil(sinks / page_size),
+ *   first) have been given back already;
+ *   free_list [P] int32, in/out: a stack, its lowest free_count[0] entries in use; free_count [1].
+ * Pages behind the window go back first: of a sequence with n_new > 0 the held logical pages in
+ * [max(first, ceil(sinks / page_size)), max(0, ctx - window + 1) / page_size), and first rises to
+ * that end (no further than the cached pages); of a finished one every page, and first is 0. They
+ * are pushed in (sequence, logical page) order. Then logical pages ceil(ctx / page_size) ..
+ * ceil((ctx + n_new) / page_size) - 1 that hold no page get one each, popped in that order.
+ * A sequence is served if its pages fit the row (max_pages), the tokens wanted by it and the
+ * sequences before it are at most max_tokens, and it needs no page or the pages needed by it and the
+ * sequences before it are at most those free. One that is not served gets no page.
+ *   cu_seqlens [N+1] int32, out: running sum of the tokens served (ctx is read only: the caller adds
+ *   them);  slot_map [max_tokens] int32, 16-byte aligned, out: the slot of each served token in that
+ *   order, -1 past the last (or where the table has no page).
+ * A sequence with ctx < 0 is left alone. The result is a fixed function of the inputs.
+ * page_size >= 1; P >= 1; max_pages >= 1; 0 <= N <= ROD_MAX_TABLE_SEQS; max_tokens >= 0;
+ * P * page_size and max_pages * page_size at most 2^31 - 1; window >= 1; sinks >= 0.
+ * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE, ROD_ERR_ALIGN, ROD_ERR_CUDA.
+ */
+#define ROD_MAX_TABLE_SEQS 16384
+ROD_API int rod_swska_page_tables(const int64_t* ctx, const int32_t* n_new, int32_t* block_table,
+                                  int32_t* first, int32_t* free_list, int32_t* free_count,
+                                  int32_t* cu_seqlens, int32_t* slot_map, int N, int max_pages, int P,
+                                  int page_size, int window, int sinks, int max_tokens, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

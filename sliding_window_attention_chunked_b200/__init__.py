@@ -20,6 +20,12 @@ the calls raise.
                                                     decode over an FP8 (E4M3) window cache
     swska_cache_fill_fp8(k, v, k_cache, v_cache, window, k_scale=1, v_scale=1)
                                                     hand-off into FP8 rings
+    swska_sink_prefill(q, k, v, window, sinks)      the attention with its first tokens always visible
+    swska_sink_backward(q, k, v, o, lse, dO, window, sinks)   its gradients
+    swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, cu_seqlens, ctx, window, sinks)
+                                                    new tokens (one to many per sequence) over a paged cache
+    swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, page_size, window, sinks, max_tokens)
+                                                    that cache's block tables and slot map
 """
 from ._binding import (  # noqa: F401
     ROD_BF16,
@@ -42,7 +48,11 @@ from ._binding import (  # noqa: F401
     swska_decode,
     swska_decode_fp8,
     swska_decode_paged,
+    swska_extend_paged,
+    swska_page_tables,
     swska_prefill,
     swska_prefill_lse,
+    swska_sink_backward,
+    swska_sink_prefill,
     test_expire_waits,
 )

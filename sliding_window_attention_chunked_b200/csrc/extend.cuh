@@ -1,0 +1,94 @@
+// extend.cuh -- work division of the paged SW-SKA attention of new tokens (swska_extend*.cu).
+//
+// A query tile is up to `rows` new tokens of one sequence; it visits the key tiles (tile keys at
+// positions that are multiples of `tile`) of the first S tokens that lie before its window, then
+// those of the window. Where the batch has fewer query tiles x head groups than the GPU has room
+// for, a tile's keys are split into units of neighbouring key tiles; each unit leaves its rows'
+// maxima, sums and unnormalised outputs in fp32, and the unit that finishes last (a counter per
+// tile and head) adds them in the order of the keys, so the result does not depend on timing.
+// The division depends on the lengths, which live on the device, so the launch that writes the new
+// tokens to the cache also makes the list of units.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace rod {
+
+struct ExtendUnit {  // 32 bytes
+    int n, q0;       // sequence, its first query of the tile
+    int kt0, kt1;    // this unit's range in the tile's list of key tiles
+    int part;        // first part of the tile (parts are numbered like units), -1: not split
+    int nsplit;
+    int split;
+    int item;        // the tile's counter row
+};
+
+struct ExtendRoute {
+    int rows = 0, tile = 0;  // queries per tile (0: route not used), keys per key tile
+    int groups = 1;          // head groups: CTAs per unit
+    int target = 1;          // units x groups to reach by splitting
+    int cap_units = 0, cap_items = 0, cap_parts = 0;
+    ExtendUnit* units = nullptr;
+    int* n_units = nullptr;
+    int* count = nullptr;    // [cap_items_split][H]
+    float* part_o = nullptr; // [cap_parts][H][rows][dv]
+    float2* part_ml = nullptr;  // [cap_parts][H][rows]
+};
+
+struct ExtendPlan {
+    ExtendRoute r[2];  // [0] sequences of at most short_len new tokens, [1] the others
+    int short_len = 0;
+};
+
+// one sequence of the batch; all arguments come from the device, so everything is bounded here
+struct ExtendSeq {
+    int row0, len;  // rows of q, k_new, v_new, o
+    int ctx;        // position of the first new token
+    bool bad;       // a position outside [0, 2^31 - len): outputs NaN
+};
+__device__ __forceinline__ ExtendSeq extend_seq(const ExtendArgs& a, int n) {
+    ExtendSeq s;
+    int lo = a.cu[n], hi = a.cu[n + 1];
+    lo = lo < 0 ? 0 : (lo > a.M ? a.M : lo);
+    hi = hi < lo ? lo : (hi > a.M ? a.M : hi);
+    s.row0 = lo;
+    s.len = hi - lo < a.max_len ? hi - lo : a.max_len;
+    const int64_t c = a.ctx[n];
+    s.bad = c < 0 || c > (int64_t)0x7fffffff - s.len;
+    s.ctx = s.bad ? 0 : (int)c;
+    return s;
+}
+
+// key tiles of the query tile [q0, q0 + rows) of a sequence
+struct ExtendKeys {
+    int n_sink, lo, n;  // tiles of the first S keys, first tile of the window, tiles in all
+    __device__ __forceinline__ int at(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+};
+__device__ __forceinline__ ExtendKeys extend_keys(const ExtendSeq& s, int q0, int rows, int tile, int W, int S) {
+    ExtendKeys k;
+    const int p0 = s.ctx + q0, last = q0 + rows < s.len ? q0 + rows : s.len;
+    const int p1 = s.ctx + last - 1;
+    const int64_t lo = (int64_t)p0 - W + 1;
+    k.lo = (int)(lo > 0 ? lo : 0) / tile;
+    const int ns = (S + tile - 1) / tile;
+    k.n_sink = ns < k.lo ? ns : k.lo;
+    k.n = k.n_sink + p1 / tile - k.lo + 1;
+    return k;
+}
+
+// The physical page of a logical page, or -1 where the table has none inside the pool.
+__device__ __forceinline__ int extend_page(const ExtendArgs& a, int n, int page) {
+    if (page < 0 || page >= a.max_pages) return -1;
+    const int e = a.table[(int64_t)n * a.max_pages + page];
+    return (unsigned)e < (unsigned)a.P ? e : -1;
+}
+
+// host: routes and workspace
+ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf16);
+size_t extend_bind(ExtendPlan& p, int H, int dv, void* workspace);  // returns the bytes
+
+// kernels; each launcher runs one route of the plan
+cudaError_t swska_extend_simt_launch(const ExtendArgs& a, const ExtendRoute& r, bool bf16, cudaStream_t s);
+
+}  // namespace rod

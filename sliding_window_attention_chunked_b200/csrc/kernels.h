@@ -136,4 +136,49 @@ cudaError_t swska_cache_fill_launch(const void* k, const void* v, void* k_cache,
                                     int H, int T, int dk, int dv, int window, size_t elem_bytes,
                                     cudaStream_t stream);
 
+// ---- SW-SKA with first tokens that stay visible ------------------------------------------------
+// streaming multiprocessors of the current device (queried once per device)
+int device_sm_count();
+
+// forward (out, lse_out) or backward (o, lse, dO -> dq, dk, dv): query t sees the keys j <= t with
+// j > t - W or j < S
+struct SinkArgs {
+    const void *q, *k, *v;       // [B,H,T,dk], [B,T,dk], [B,H,T,dv]
+    void* out;                   // forward: [B,H,T,dv]
+    float* lse_out;              // forward: [B,H,T]
+    const void* o;               // backward: the forward's output and log-sum-exp
+    const float* lse;
+    const void* dO;
+    void *dq, *dk, *dv;
+    int B, H, T, d_k, d_v, W, S;  // W clamped to T
+    float scale;
+    void* workspace;
+};
+cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
+cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
+cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
+cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
+size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S);
+
+// block tables, free list and slot map from cached and new lengths
+constexpr int kMaxTableSeqs = 16384;
+cudaError_t swska_page_tables_launch(const int64_t* ctx, const int32_t* n_new, int32_t* table, int32_t* first,
+                                     int32_t* free_list, int32_t* free_count, int32_t* cu, int32_t* slot, int N,
+                                     int max_pages, int P, int page, int W, int S, int M, cudaStream_t stream);
+
+// attention of a ragged batch of new tokens over a paged cache
+struct ExtendArgs {
+    const void *q, *k_new, *v_new;  // [M,H,dk], [M,dk], [M,H,dv]; k_new null: nothing is written
+    void *k_pool, *v_pool;          // [P][page][dk], [P][H][page][dv]
+    const int32_t *table, *slot, *cu;
+    const int64_t* ctx;
+    void* o;                        // [M,H,dv]
+    int M, N, H, d_k, d_v, P, page, max_pages, W, S, max_len;
+    float scale;
+    void* workspace;
+    int es;                         // bytes of an element
+};
+size_t swska_extend_workspace_size(int M, int N, int H, int dk, int dv, int max_len, bool bf16);
+cudaError_t swska_extend_launch(const ExtendArgs& a, bool bf16, cudaStream_t s);
+
 }  // namespace rod

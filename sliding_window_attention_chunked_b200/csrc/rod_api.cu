@@ -11,6 +11,16 @@
 namespace rod {
 static std::atomic<uint64_t> g_launches{0};
 void note_launches(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
+
+int device_sm_count() {
+    static std::atomic<int> cache[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if ((sms = cache[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 148;
+    cache[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
 }  // namespace rod
 
 namespace {
@@ -18,6 +28,7 @@ namespace {
 thread_local int t_last_cuda_error = 0;
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool dtype_ok(int dt) { return dt == ROD_BF16 || dt == ROD_FP32; }
 
@@ -326,6 +337,113 @@ int rod_swska_cache_fill_fp8(const void* k, const void* v, void* k_cache, void* 
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return ROD_ERR_ALIGN;
     return from_cuda(rod::swska_cache_fill_fp8_launch(k, v, k_cache, v_cache, B, H, T, dk, dv, window, k_scale,
                                                       v_scale, static_cast<cudaStream_t>(stream)));
+}
+
+int rod_swska_sink_prefill(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T,
+                           int dk, int dv, int window, int sinks, float scale, int dtype, void* stream) {
+    if (!dtype_ok(dtype)) return ROD_ERR_DTYPE;
+    if (B < 0 || H < 0 || T < 0 || H > 64 || window < 1 || sinks < 0 || sinks > ROD_MAX_SINKS || !dim_ok(dk) ||
+        !dim_ok(dv))
+        return ROD_ERR_SHAPE;
+    if (!(scale == scale) || isinf(scale)) return ROD_ERR_SHAPE;
+    if ((int64_t)B * H == 0 || T == 0) return ROD_OK;
+    if (!q || !k || !v || !o || !lse) return ROD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned_to(lse, 4)) return ROD_ERR_ALIGN;
+    rod::SinkArgs a{};
+    a.q = q, a.k = k, a.v = v, a.out = o, a.lse_out = lse;
+    a.B = B, a.H = H, a.T = T, a.d_k = dk, a.d_v = dv, a.W = window < T ? window : T, a.S = sinks;
+    a.scale = resolve_scale(scale, dk);
+    return from_cuda(rod::swska_sink_prefill_launch(a, dtype == ROD_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rod_swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int window, int sinks) {
+    if (B < 0 || H < 0 || T < 0 || H > 64 || window < 1 || sinks < 0 || sinks > ROD_MAX_SINKS || !dim_ok(dk) ||
+        !dim_ok(dv))
+        return 0;
+    if ((int64_t)B * H == 0 || T == 0) return 0;
+    return rod::swska_sink_backward_workspace_size(B, H, T, dk, dv, window < T ? window : T, sinks);
+}
+
+int rod_swska_sink_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                            const void* dO, void* dq, void* dk, void* dv, int B, int H, int T, int dk_dim, int dv_dim,
+                            int window, int sinks, float scale, int dtype, void* workspace, size_t ws_bytes,
+                            void* stream) {
+    if (!dtype_ok(dtype)) return ROD_ERR_DTYPE;
+    if (B < 0 || H < 0 || T < 0 || H > 64 || window < 1 || sinks < 0 || sinks > ROD_MAX_SINKS || !dim_ok(dk_dim) ||
+        !dim_ok(dv_dim))
+        return ROD_ERR_SHAPE;
+    if (!(scale == scale) || isinf(scale)) return ROD_ERR_SHAPE;
+    if ((int64_t)B * H == 0 || T == 0) return ROD_OK;
+    if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return ROD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned_to(lse, 4) || !aligned16(dO) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+        return ROD_ERR_ALIGN;
+    if (!workspace || ws_bytes < rod_swska_sink_backward_workspace_size(B, H, T, dk_dim, dv_dim, window, sinks))
+        return ROD_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ROD_ERR_ALIGN;
+    rod::SinkArgs a{};
+    a.q = q, a.k = k, a.v = v, a.o = o, a.lse = lse, a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
+    a.B = B, a.H = H, a.T = T, a.d_k = dk_dim, a.d_v = dv_dim, a.W = window < T ? window : T, a.S = sinks;
+    a.scale = resolve_scale(scale, dk_dim);
+    a.workspace = workspace;
+    return from_cuda(rod::swska_sink_backward_launch(a, dtype == ROD_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rod_swska_extend_paged_workspace_size(int M, int N, int H, int dk, int dv, int max_len, int dtype) {
+    if (M < 0 || N < 0 || N > ROD_MAX_EXTEND_SEQS || H < 1 || H > 64 || max_len < 0 || !dim_ok(dk) || !dim_ok(dv) ||
+        !dtype_ok(dtype))
+        return 0;
+    if (M == 0 || N == 0) return 0;
+    return rod::swska_extend_workspace_size(M, N, H, dk, dv, max_len > 0 ? max_len : M, dtype == ROD_BF16);
+}
+
+int rod_swska_extend_paged(const void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                           const int32_t* block_table, const int32_t* slot_map, const int32_t* cu_seqlens,
+                           const int64_t* ctx, void* o, int M, int N, int H, int dk, int dv, int P, int page_size,
+                           int max_pages, int window, int sinks, int max_len, float scale, int dtype,
+                           void* workspace, size_t ws_bytes, void* stream) {
+    if (!dtype_ok(dtype)) return ROD_ERR_DTYPE;
+    if (M < 0 || N < 0 || N > ROD_MAX_EXTEND_SEQS || H < 1 || H > 64 || !dim_ok(dk) || !dim_ok(dv) || P < 1 ||
+        page_size < 8 || page_size % 8 != 0 || max_pages < 1 || (int64_t)P * page_size > INT32_MAX ||
+        (int64_t)max_pages * page_size > INT32_MAX || window < 1 || sinks < 0 || sinks > ROD_MAX_SINKS || max_len < 0)
+        return ROD_ERR_SHAPE;
+    if (!(scale == scale) || isinf(scale)) return ROD_ERR_SHAPE;
+    if (M == 0 || N == 0) return ROD_OK;
+    if (!q || !k_pool || !v_pool || !block_table || !cu_seqlens || !ctx || !o) return ROD_ERR_NULL;
+    if ((k_new != nullptr) != (v_new != nullptr) || (k_new != nullptr) != (slot_map != nullptr)) return ROD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned16(k_new) ||
+        !aligned16(v_new) || !aligned_to(ctx, 8) || !aligned_to(block_table, 4) || !aligned_to(slot_map, 4) ||
+        !aligned_to(cu_seqlens, 4))
+        return ROD_ERR_ALIGN;
+    if (!workspace || ws_bytes < rod_swska_extend_paged_workspace_size(M, N, H, dk, dv, max_len, dtype))
+        return ROD_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ROD_ERR_ALIGN;
+    rod::ExtendArgs a{};
+    a.q = q, a.k_new = k_new, a.v_new = v_new, a.k_pool = k_pool, a.v_pool = v_pool, a.table = block_table;
+    a.slot = slot_map, a.cu = cu_seqlens, a.ctx = ctx, a.o = o;
+    a.M = M, a.N = N, a.H = H, a.d_k = dk, a.d_v = dv, a.P = P, a.page = page_size, a.max_pages = max_pages;
+    a.W = window, a.S = sinks, a.max_len = max_len > 0 && max_len < M ? max_len : M;
+    a.scale = resolve_scale(scale, dk);
+    a.workspace = workspace;
+    a.es = dtype == ROD_BF16 ? 2 : 4;
+    return from_cuda(rod::swska_extend_launch(a, dtype == ROD_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int rod_swska_page_tables(const int64_t* ctx, const int32_t* n_new, int32_t* block_table, int32_t* first,
+                          int32_t* free_list, int32_t* free_count, int32_t* cu_seqlens, int32_t* slot_map, int N,
+                          int max_pages, int P, int page_size, int window, int sinks, int max_tokens, void* stream) {
+    if (N < 0 || N > ROD_MAX_TABLE_SEQS || max_pages < 1 || P < 1 || page_size < 1 || window < 1 || sinks < 0 ||
+        max_tokens < 0 || (int64_t)P * page_size > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX)
+        return ROD_ERR_SHAPE;
+    if (!free_list || !free_count || !cu_seqlens) return ROD_ERR_NULL;
+    if (N > 0 && (!ctx || !n_new || !block_table || !first)) return ROD_ERR_NULL;
+    if (max_tokens > 0 && !slot_map) return ROD_ERR_NULL;
+    if (!aligned_to(ctx, 8) || !aligned_to(n_new, 4) || !aligned_to(block_table, 4) || !aligned_to(first, 4) ||
+        !aligned_to(free_list, 4) || !aligned_to(free_count, 4) || !aligned_to(cu_seqlens, 4) || !aligned16(slot_map))
+        return ROD_ERR_ALIGN;
+    return from_cuda(rod::swska_page_tables_launch(ctx, n_new, block_table, first, free_list, free_count, cu_seqlens,
+                                                   slot_map, N, max_pages, P, page_size, window, sinks, max_tokens,
+                                                   static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,92 @@
+// sink_parts.cu -- host side and reduction launch of sink_parts.cuh.
+#include "sink_parts.cuh"
+
+#include "simt_tile.cuh"
+
+namespace rod {
+namespace {
+
+// Memory bound: reads every part once, writes dk (and the S rows of dv) once.
+__global__ void __launch_bounds__(256)
+sink_reduce_kernel(const SinkParts p, void* __restrict__ dk, void* __restrict__ dv, bool bf16, float scale) {
+    const int64_t n_dk = (int64_t)p.B * p.T * p.dk / 4;
+    const int64_t n_dv = p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_dk + n_dv;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float* x) {
+            const float4 t = *reinterpret_cast<const float4*>(x);
+            s.x += t.x;
+            s.y += t.y;
+            s.z += t.z;
+            s.w += t.w;
+        };
+        if (i < n_dk) {
+            const int64_t row = 4 * i / p.dk;
+            const int c = (int)(4 * i - row * p.dk), b = (int)(row / p.T), key = (int)(row % p.T);
+            for (int g = 0; g < p.G; ++g) add(p.dk_part + (int64_t)g * n_dk * 4 + 4 * i);
+            if (p.nseg > 0 && key < p.R)
+                for (int sl = 1; sl <= p.nseg; ++sl)
+                    for (int g = 0; g < p.G; ++g) add(p.dk_at(sl, g, b, key) + c);
+            simt::store4_as(dk, bf16, 4 * i, make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale));
+        } else {
+            const int64_t e = 4 * (i - n_dk), row = e / p.dv;
+            const int c = (int)(e - row * p.dv), key = (int)(row % p.R);
+            const int64_t bh = row / p.R;
+            for (int sl = 0; sl <= p.nseg; ++sl) add(p.dv_at(sl, bh, key) + c);
+            simt::store4_as(dv, bf16, (bh * p.T + key) * p.dv + c, s);
+        }
+    }
+}
+
+int64_t tpad(int T) { return ((int64_t)T + 127) / 128 * 128; }
+
+}  // namespace
+
+SinkParts sink_parts_plan(const SinkArgs& a, int size, int G) {
+    SinkParts p;
+    p.G = G;
+    p.B = a.B;
+    p.H = a.H;
+    p.T = a.T;
+    p.dk = a.d_k;
+    p.dv = a.d_v;
+    p.R = a.S < a.T ? a.S : a.T;
+    const int tiles = (a.T + size - 1) / size;
+    const int far = tiles - 1 - SinkParts::near_hi(0, tiles, size, a.W);  // the first tile has the most
+    if (p.R > 0 && far > 0) {
+        const int near = SinkParts::near_hi(0, tiles, size, a.W) + 1;
+        p.n_tiles = (p.R + size - 1) / size;
+        // a segment is a window long, at least 4 tiles (its sums are S rows of memory traffic), and
+        // there are at most 64 of them
+        p.seg_len = near > 4 ? near : 4;
+        if (p.seg_len * 64 < far) p.seg_len = (far + 63) / 64;
+        p.nseg = (far + p.seg_len - 1) / p.seg_len;
+    }
+    return p;
+}
+
+size_t sink_parts_floats(const SinkParts& p) {
+    const size_t bh = (size_t)p.B * p.H;
+    size_t n = 2 * bh * (size_t)tpad(p.T) + (size_t)p.G * p.B * p.T * p.dk;
+    if (p.nseg > 0) n += (size_t)(1 + p.nseg) * bh * p.R * p.dv + (size_t)p.nseg * p.G * p.B * p.R * p.dk;
+    return n;
+}
+
+float* sink_parts_bind(SinkParts& p, const SinkArgs& a) {
+    float* ws = static_cast<float*>(a.workspace);
+    p.dk_part = ws + 2 * (size_t)p.B * p.H * tpad(p.T);
+    p.dv_far = p.dk_part + (size_t)p.G * p.B * p.T * p.dk;
+    p.dk_far = p.dv_far + (p.nseg > 0 ? (size_t)(1 + p.nseg) * p.B * p.H * p.R * p.dv : 0);
+    return ws;
+}
+
+cudaError_t sink_parts_reduce(const SinkParts& p, const SinkArgs& a, bool bf16, cudaStream_t s) {
+    const int64_t n = (int64_t)p.B * p.T * p.dk / 4 + (p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0);
+    const int64_t want = (n + 255) / 256, cap = 8 * (int64_t)device_sm_count();
+    sink_reduce_kernel<<<(unsigned)(want < cap ? want : cap), 256, 0, s>>>(p, a.dk, a.dv, bf16, a.scale);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace rod

@@ -1,0 +1,337 @@
+// swska_sink_simt.cu -- SW-SKA with first tokens that stay visible, forward and backward on CUDA
+// cores (every product an fp32 FMA): fp32 inputs, and bf16 shapes outside the tensor-core kernels.
+//
+// Query t sees the keys j <= t with j > t - W or j < S:
+//   p_tj = softmax_j(scale q_t . k_j),  o_t = sum_j p_tj v_j,  lse_t = log sum_j exp(scale q_t . k_j)
+//   D_t = dO_t . o_t,  dS_tj = p_tj (dO_t . v_j - D_t)
+//   dq_t = scale sum_j dS_tj k_j,  dv_j = sum_t p_tj dO_t,  dk_j = scale sum_h sum_t dS_tj q_t
+// One CTA per 64 queries of a head (forward, dq) or per 64 keys of a head (dk, dv), with the
+// tiles of simt_tile.cuh; it visits the tiles that its rows can see and masks inside them. The
+// kernels are bound by FMA issue: a 64 x 64 tile of head dim 128 is 1 M FMAs per product against 64 KB
+// of tile loads that stay in L2.
+//
+// A key tile among the first S is seen by every later query, up to T / W times the work of another
+// tile. Its queries past the window are dealt out in segments to further CTAs, each with its own
+// partial sums for the S rows; the last launch adds the parts in a fixed order, so the result does
+// not depend on timing. The same launch adds the heads' parts of the shared dk.
+#include <math.h>
+
+#include "kernels.h"
+#include "simt_tile.cuh"
+#include "sink_parts.cuh"
+
+namespace rod {
+namespace {
+
+using namespace simt;
+
+constexpr int BQ = 64;
+constexpr int NTH = 4 * BQ;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int DK, int DV>
+constexpr int fwd_smem() { return (BQ * ld<DK>() + BK * ld<DK>() + BK * ld<DV>() + BQ * LDP) * 4; }
+
+// key tiles of a query tile: those of the first S keys that lie before the window's, then the window's
+struct KeyTiles {
+    int n_sink, lo, n;
+    __device__ __forceinline__ int at(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int W, int S) {
+    KeyTiles k;
+    k.lo = (t0 - W + 1 > 0 ? t0 - W + 1 : 0) / BK;
+    const int ns = (S + BK - 1) / BK;
+    k.n_sink = ns < k.lo ? ns : k.lo;
+    k.n = k.n_sink + t1 / BK - k.lo + 1;
+    return k;
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(NTH)
+sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
+                void* __restrict__ o, float* __restrict__ lse, bool bf16, int H, int T, int W, int S, float scale_log2,
+                int qtiles) {
+    extern __shared__ __align__(16) float sm[];
+    float* sQ = sm;
+    float* sK = sQ + BQ * ld<DK>();
+    float* sV = sK + BK * ld<DK>();
+    float* sP = sV + BK * ld<DV>();
+    const int64_t bh = blockIdx.x / qtiles, b = bh / H;
+    const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
+    load_tile<DK, BQ, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    const KeyTiles kt = key_tiles(t0, t1, W, S);
+    float m[4], l[4], acc[4][DV / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) acc[i][c] = 0.f;
+    }
+    for (int it = 0; it < kt.n; ++it) {
+        const int key0 = kt.at(it) * BK;
+        __syncthreads();
+        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; });
+        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+        __syncthreads();
+        float s[4][4];
+        tile_dot<DK>(sQ, sK, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[i][j] = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S) ? s[i][j] * scale_log2 : -INFINITY;
+        softmax_step<DV / 16>(s, m, l, acc);
+        put_tile(sP, ty, tx, s);
+        __syncthreads();
+        tile_mul<DV>(sP, sV, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * ty + i;
+        if (t >= T) continue;
+        const float inv = 1.f / l[i];
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c)
+            store1_as(o, bf16, (bh * T + t) * (int64_t)DV + Cols<DV>::at(tx, c), acc[i][c] * inv);
+        if (tx == 0) lse[bh * T + t] = (m[i] + log2f(l[i])) * kLn2;
+    }
+}
+
+template <int DK, int DV>
+constexpr int dq_smem() { return (BQ * (ld<DK>() + ld<DV>()) + BK * (ld<DK>() + ld<DV>()) + BQ * LDP) * 4; }
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(NTH)
+sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
+               const void* __restrict__ o, const float* __restrict__ lse, const void* __restrict__ dO,
+               void* __restrict__ dq, float* __restrict__ dbuf, bool bf16, int H, int T, int W, int S, float scale,
+               int qtiles) {
+    extern __shared__ __align__(16) float sm[];
+    float* sQ = sm;
+    float* sG = sQ + BQ * ld<DK>();
+    float* sK = sG + BQ * ld<DV>();
+    float* sV = sK + BK * ld<DK>();
+    float* sP = sV + BK * ld<DV>();
+    const int64_t bh = blockIdx.x / qtiles, b = bh / H;
+    const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
+    const float scale_log2 = scale * kLog2e;
+    load_tile<DK, BQ, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    load_tile<DV, BQ, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
+    __syncthreads();
+    float L2[4], D[4], acc[4][DK / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, t = t0 + r;
+        float d = 0.f;
+        if (t < T)
+            for (int c = tx; c < DV; c += 16) {
+                const int64_t at = (bh * T + t) * (int64_t)DV + c;
+                const float ov = bf16 ? to_f32(static_cast<const __nv_bfloat16*>(o)[at]) : static_cast<const float*>(o)[at];
+                d = fmaf(sG[r * ld<DV>() + c], ov, d);
+            }
+        D[i] = row_sum(d);
+        L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
+        if (tx == 0 && t < T) dbuf[bh * T + t] = D[i];
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) acc[i][c] = 0.f;
+    }
+    const KeyTiles kt = key_tiles(t0, t1, W, S);
+    for (int it = 0; it < kt.n; ++it) {
+        const int key0 = kt.at(it) * BK;
+        __syncthreads();
+        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; });
+        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+        __syncthreads();
+        float s[4][4], g[4][4];
+        tile_dot<DK>(sQ, sK, ty, tx, s);
+        tile_dot<DV>(sG, sV, ty, tx, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool see = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S);
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) * (g[i][j] - D[i]) : 0.f;
+            }
+        put_tile(sP, ty, tx, s);
+        __syncthreads();
+        tile_mul<DK>(sP, sK, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * ty + i;
+        if (t >= T) continue;
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c)
+            store1_as(dq, bf16, (bh * T + t) * (int64_t)DK + Cols<DK>::at(tx, c), acc[i][c] * scale);
+    }
+}
+
+template <int DK, int DV>
+constexpr int dkv_smem() {
+    return (2 * BK * (ld<DK>() + ld<DV>()) + BK * LDP + 2 * BK) * 4;
+}
+
+// blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
+template <int DK, int DV>
+__global__ void __launch_bounds__(NTH)
+sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
+                const float* __restrict__ lse, const float* __restrict__ dbuf, const void* __restrict__ dO,
+                void* __restrict__ dv, SinkParts parts, bool bf16, int B, int H, int T, int W, int S, float scale,
+                int tiles) {
+    extern __shared__ __align__(16) float sm[];
+    float* sK = sm;
+    float* sV = sK + BK * ld<DK>();
+    float* sQ = sV + BK * ld<DV>();
+    float* sG = sQ + BK * ld<DK>();
+    float* sP = sG + BK * ld<DV>();
+    float* sL = sP + BK * LDP;
+    float* sD = sL + BK;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int64_t bh = (int64_t)b * H + h;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const SinkWork w = parts.work((int)blockIdx.x, tiles, BK, T, W);
+    const int key0 = w.tile * BK;
+    load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
+    load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    const float scale_log2 = scale * kLog2e;
+    float ak[4][DK / 16], av[4][DV / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) ak[i][c] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) av[i][c] = 0.f;
+    }
+    for (int qt = w.q_lo; qt <= w.q_hi; ++qt) {
+        const int t0 = qt * BK;
+        __syncthreads();
+        load_tile<DK, BK, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+        load_tile<DV, BK, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
+        for (int r = threadIdx.x; r < BK; r += NTH) {
+            sL[r] = t0 + r < T ? lse[bh * T + t0 + r] * kLog2e : INFINITY;
+            sD[r] = t0 + r < T ? dbuf[bh * T + t0 + r] : 0.f;
+        }
+        __syncthreads();
+        float s[4][4], g[4][4];  // rows: keys, columns: queries
+        tile_dot<DK>(sK, sQ, ty, tx, s);
+        tile_dot<DV>(sV, sG, ty, tx, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j;
+                const bool see = ska_visible(t0 + c, key0 + 4 * ty + i, W, S);
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -sL[c])) : 0.f;
+                g[i][j] = s[i][j] * (g[i][j] - sD[c]);
+            }
+        put_tile(sP, ty, tx, s);
+        __syncthreads();
+        tile_mul<DV>(sP, sG, ty, tx, av);
+        __syncthreads();
+        put_tile(sP, ty, tx, g);
+        __syncthreads();
+        tile_mul<DK>(sP, sQ, ty, tx, ak);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int key = key0 + 4 * ty + i;
+        if (key >= T) continue;
+        const bool part = parts.nseg > 0 && key < S;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) {
+            const int col = Cols<DV>::at(tx, c);
+            if (part) parts.dv_at(w.slot, bh, key)[col] = av[i][c];
+            else if (w.slot == 0) store1_as(dv, bf16, (bh * T + key) * (int64_t)DV + col, av[i][c]);
+        }
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) {
+            const int col = Cols<DK>::at(tx, c);
+            if (w.slot == 0) parts.dk_part[(((int64_t)h * B + b) * T + key) * DK + col] = ak[i][c];
+            else if (part) parts.dk_at(w.slot, h, b, key)[col] = ak[i][c];
+        }
+    }
+}
+
+template <int DK, int DV>
+cudaError_t fwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    const int qtiles = (a.T + BQ - 1) / BQ;
+    const int64_t grid = (int64_t)qtiles * a.B * a.H;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         fwd_smem<DK, DV>());
+    if (e != cudaSuccess) return e;
+    sink_fwd_kernel<DK, DV><<<(unsigned)grid, NTH, fwd_smem<DK, DV>(), s>>>(
+        a.q, a.k, a.v, a.out, a.lse_out, bf16, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+template <int DK, int DV>
+cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    const int tiles = (a.T + BQ - 1) / BQ;
+    const int64_t grid = (int64_t)tiles * a.B * a.H;
+    if (grid > 0x7fffffffLL || a.B > 65535) return cudaErrorInvalidConfiguration;
+    SinkParts parts = sink_parts_plan(a, BK, a.H);
+    float* dbuf = sink_parts_bind(parts, a);
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(sink_dq_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  dq_smem<DK, DV>())) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  dkv_smem<DK, DV>())) != cudaSuccess)
+        return e;
+    sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH, dq_smem<DK, DV>(), s>>>(
+        a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, bf16, a.H, a.T, a.W, a.S, a.scale, tiles);
+    sink_dkv_kernel<DK, DV><<<dim3((unsigned)(tiles + parts.n_tiles * parts.nseg), (unsigned)a.H, (unsigned)a.B), NTH,
+                              dkv_smem<DK, DV>(), s>>>(a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H,
+                                                       a.T, a.W, a.S, a.scale, tiles);
+    note_launches(2);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return sink_parts_reduce(parts, a, bf16, s);
+}
+
+template <int DK>
+cudaError_t pick_dv(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    switch (a.d_v) {
+        case 16: return backward ? bwd_t<DK, 16>(a, bf16, s) : fwd_t<DK, 16>(a, bf16, s);
+        case 32: return backward ? bwd_t<DK, 32>(a, bf16, s) : fwd_t<DK, 32>(a, bf16, s);
+        case 64: return backward ? bwd_t<DK, 64>(a, bf16, s) : fwd_t<DK, 64>(a, bf16, s);
+        case 128: return backward ? bwd_t<DK, 128>(a, bf16, s) : fwd_t<DK, 128>(a, bf16, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t pick(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    switch (a.d_k) {
+        case 16: return pick_dv<16>(a, bf16, backward, s);
+        case 32: return pick_dv<32>(a, bf16, backward, s);
+        case 64: return pick_dv<64>(a, bf16, backward, s);
+        case 128: return pick_dv<128>(a, bf16, backward, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, false, s); }
+cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, true, s); }
+
+cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    return swska_sink_prefill_simt_launch(a, bf16, s);
+}
+cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    return swska_sink_backward_simt_launch(a, bf16, s);
+}
+size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S) {
+    SinkArgs a{};
+    a.B = B, a.H = H, a.T = T, a.d_k = dk, a.d_v = dv, a.W = W, a.S = S;
+    return sink_parts_floats(sink_parts_plan(a, BK, H)) * sizeof(float);
+}
+
+}  // namespace rod
