@@ -48,11 +48,12 @@ unsigned swska_prefill_tc_take_timeout_flag();
 // the same kernel with per-row statistics: lse_mul * (base-2 log-sum-exp) into row bh * Tpad + t
 // of `lse` (-1 gives the backward's negated base-2 form, ln 2 the natural log-sum-exp; rows past
 // T, up to Tpad, get -inf) and, with dO given, D = dO . o into the same row of dbuf. o may be
-// null (the output is then not stored), and so may dO and dbuf.
+// null (the output is then not stored), and so may dO and dbuf. sinks > 0 (with lse): the first
+// tokens that stay visible to every query.
 cudaError_t swska_prefill_tc_stats_launch(const void* q, const void* k, const void* v, void* o,
                                           const void* dO, float* lse, float* dbuf, int64_t Tpad, int B,
                                           int H, int T, int window, float scale, cudaStream_t stream,
-                                          float lse_mul = -1.f);
+                                          float lse_mul = -1.f, int sinks = 0);
 
 
 // TMA descriptors for a 3-D tensor [d2][d1][d0] loaded as boxes of box1 x box0 elements
@@ -156,6 +157,7 @@ struct SinkArgs {
 };
 cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
 cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
+cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t s);  // bf16, dk = dv = 128, T >= 128
 cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
 cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
 size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S);

@@ -38,6 +38,7 @@
 #include "common.cuh"
 #include "exp2x2.cuh"
 #include "kernels.h"
+#include "sink_parts.cuh"
 #include "tc.cuh"
 
 namespace rod {
@@ -128,6 +129,14 @@ __device__ __forceinline__ void mask_chunk(uint32_t* s, int c, int lo, int hi) {
         if (col < lo || col > hi) s[e] = 0xff800000u;
     }
 }
+// the same with the columns before `first` (the first tokens) kept
+__device__ __forceinline__ void mask_chunk_first(uint32_t* s, int c, int lo, int hi, int first) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        const int col = 32 * c + e;
+        if ((col < lo && col >= first) || col > hi) s[e] = 0xff800000u;
+    }
+}
 // Which groups of four exponentials in a 32-column chunk go to the FMA pipe (bit g: columns
 // 4 g .. 4 g + 3); the rest use the SFU.
 constexpr unsigned kPolyGroups = 0xAAu;
@@ -147,6 +156,10 @@ constexpr int NBAR = 2 * KSLOT + 2 * VSLOT + 7;
 constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
+// with first tokens: one more barrier (decided) and each row's two half sums
+constexpr int OFF_SUMS = OFF_MISC + 32;
+constexpr int SMEM_SINK = OFF_SUMS + 2 * TILE * 4 + 1024;
+static_assert(SMEM_SINK <= 232448, "shared memory");
 }  // namespace qa
 
 // TMEM columns: S buffers at 0 and 384 (tile u uses buffer u & 1), dP at 128, dQ at 256.
@@ -155,12 +168,20 @@ __device__ __forceinline__ uint32_t s_col(int u) { return (u & 1) ? 384u : 0u; }
 // columns sit, two per 32-bit column, in columns 64 w .. 64 w + 31 of the S buffer
 __device__ __forceinline__ uint32_t packed_col(int k) { return (uint32_t)(8 * k + (k >= 4 ? 32 : 0)); }
 
+// SINK: the first S tokens stay visible to every query; their key tile comes before the window's.
+// There D = dbuf comes from the stored bf16 o, off by about 2^-9 of it. Where a row's attention is
+// peaked, dS = p (dP - D) of the peak is a small difference and that error would show. So the sweep
+// also sums e = sum_j p_j (dP_j - D) of each row in fp32, D + e (the row's own sum p dP) goes back to
+// dbuf for the key-tile kernel, and a CTA with a peaked row (sum of p^2 over half the columns above
+// 1/8, so above 1/4 in all) sweeps its tiles once more with it. Rows that see few keys always are
+// (the first tile, short windows: a sweep of few tiles); for long windows only peaked ones are.
+template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   __nv_bfloat16* __restrict__ dq, const float* __restrict__ nlse2,
-                  const float* __restrict__ dbuf, int T, int Tpad, int H, int W, float scale_log2,
-                  float scale, int n_qtiles) {
+                  float* __restrict__ dbuf, int T, int Tpad, int H, int W, float scale_log2,
+                  float scale, int n_qtiles, int S_arg) {
     using namespace qa;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024(smem_raw);
@@ -170,7 +191,10 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int bh = b * H + h;
     const int t0 = qt * TILE;
     const int kt_lo = (t0 - W + 1 > 0 ? t0 - W + 1 : 0) / TILE;
-    const int n_it = qt - kt_lo + 1;  // key tiles of the window
+    const int S = SINK ? S_arg : 0;
+    const int n_sink = min((S + TILE - 1) / TILE, kt_lo);
+    const int n_it = qt - kt_lo + 1 + n_sink;  // key tiles of the first tokens and of the window
+    auto key_tile = [&](int i) { return i < n_sink ? i : kt_lo + i - n_sink; };
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* kfull = bars;
@@ -185,8 +209,14 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     uint64_t* drain = done + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+    volatile int* redo = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);   // SINK: sweep again
+    uint64_t* decided = reinterpret_cast<uint64_t*>(smem + OFF_MISC + 16);       // SINK: redo is set
 
     if (threadIdx.x == 0) {
+        if (SINK) {
+            mbar_init(decided, 1);
+            *redo = 0;
+        }
         for (int i = 0; i < KSLOT; ++i) {
             mbar_init(&kfull[i], 1);
             mbar_init(&kempty[i], 1);
@@ -227,8 +257,9 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc::tma_load_3d(smem + OFF_DO + half * BOX_BYTES, &tm_do, half * 64, t0, bh, qfull);
             }
             int nk = 0, nv = 0;  // loads started
-            for (int u = 0; u < n_it; ++u) {  // K(u) then V(u), each into its own ring
-                const int key0 = (kt_lo + u) * TILE;
+            for (int u = 0; u < (SINK ? 2 * n_it : n_it); ++u) {  // K(u) then V(u), each into its own ring
+                if (SINK && u == n_it && (!wait_bar(decided, 0, abort_flag) || !*redo)) break;
+                const int key0 = key_tile(SINK && u >= n_it ? u - n_it : u) * TILE;
                 const int ks = u % KSLOT, vs = u % VSLOT;
                 if (u >= KSLOT && !wait_bar(&kempty[ks], (uint32_t)((u / KSLOT - 1) & 1), abort_flag)) break;
                 mbar_arrive_expect_tx(&kfull[ks], TILE_BYTES);
@@ -286,36 +317,41 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             tc::mma_commit_warp(pfull);
             tc::mma_commit_warp(&vempty[u % VSLOT]);
         };
+        int u0 = 0;  // the sweep's first tile
         auto issue_dq = [&](int u) {  // dQ += dS(u) K(u); K(u) is free once it completes
             const uint32_t k_lo = lo_mnmajor(kslot(u));
 #pragma unroll
             for (int k = 0; k < TILE / 16; ++k)
                 tc::mma_ts_lh_warp(tmem + 256u, tmem + s_col(u) + packed_col(k), k_lo + mnstep(k), d_hi, idesc_g,
-                                   (u > 0 || k > 0) ? 1u : 0u);
+                                   (u > u0 || k > 0) ? 1u : 0u);
             tc::mma_commit_warp(&kempty[u % KSLOT]);
         };
         ok = wait_bar_warp(qfull, 0, abort_flag);
         tc::fence_after_sync();
-        if (ok && acq_k(0)) {
+        for (; ok && acq_k(u0); u0 = n_it) {
+            const int u1 = u0 + n_it;
             // order: S(0) dP(0) S(1) | dQ(0) dP(1) S(2) | dQ(1) dP(2) S(3) | ...
-            issue_s(0);
-            if (acq_v(0)) issue_dp(0);
-            if (ok && n_it > 1 && acq_k(1)) issue_s(1);
-            for (int u = 0; u < n_it && ok; ++u) {
+            issue_s(u0);
+            if (acq_v(u0)) issue_dp(u0);
+            if (ok && n_it > 1 && acq_k(u0 + 1)) issue_s(u0 + 1);
+            for (int u = u0; u < u1 && ok; ++u) {
                 if (!wait_bar_warp(dsready, (uint32_t)(u & 1), abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
                 issue_dq(u);
-                if (u + 1 < n_it) {
+                if (u + 1 < u1) {
                     if (!acq_v(u + 1)) break;
                     issue_dp(u + 1);
                 }
-                if (u + 2 < n_it) {
+                if (u + 2 < u1) {
                     if (!acq_k(u + 2)) break;
                     issue_s(u + 2);  // into the buffer dQ(u) is reading: the pipe runs in order
                 }
             }
-            if (ok) tc::mma_commit_warp(done);
+            if (!SINK || u0 > 0 || !ok) break;
+            ok = wait_bar_warp(decided, 0, abort_flag);
+            if (!ok || !*redo) break;
         }
+        if (ok) tc::mma_commit_warp(done);
         // every MMA this warp issued has completed before TMEM is released
         tc::mma_commit_warp(drain);
         mbar_wait_bounded(drain, 0, kWaitLimit);
@@ -328,14 +364,18 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t tQ = tmem + lane_base + 256u + 64u * w;
         const int t = t0 + row;
         const float nL = nlse2[(int64_t)bh * Tpad + t];  // -inf past the end: p = 0
-        const float Dr = dbuf[(int64_t)bh * Tpad + t];
+        float Dr = dbuf[(int64_t)bh * Tpad + t];
         const float2 sl2 = make_float2(scale_log2, scale_log2), nl2 = make_float2(nL, nL);
-        const float2 d2 = make_float2(Dr, Dr);
+        float2 d2 = make_float2(Dr, Dr);
+        float2 e2 = make_float2(0.f, 0.f), pp2 = make_float2(0.f, 0.f);  // SINK: sums of dS and p^2
         bool ok = true;
-        for (int u = 0; u < n_it; ++u) {
+        int u_end = n_it;
+        bool met = false;  // SINK: the softmax warps' meeting after the first sweep
+        for (int u = 0; u < u_end; ++u) {
             const uint32_t tS = tmem + lane_base + s_col(u) + 64u * w;
-            const int key0 = (kt_lo + u) * TILE + HALF * w;  // first key of this half
-            const bool full_tile = key0 >= t0 + TILE - W && key0 + HALF - 1 <= t0;
+            const int key0 = key_tile(SINK && u >= n_it ? u - n_it : u) * TILE + HALF * w;  // first key of this half
+            const bool full_tile =
+                (key0 >= t0 + TILE - W || (SINK && key0 + HALF <= S)) && key0 + HALF - 1 <= t0;
             const int lo = t - W + 1 - key0, hi = t - key0;   // valid columns [lo, hi]
             // phase 1: P from S
             if (!wait_bar_warp(&sfull[u & 1], (uint32_t)((u >> 1) & 1), abort_flag)) { ok = false; break; }
@@ -346,7 +386,10 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 uint32_t s[32];
                 tc::tmem_ld32(tS + 32u * c, s);
                 tc::tmem_wait_ld();
-                if (!full_tile) mask_chunk(s, c, lo, hi);
+                if (!full_tile) {
+                    if (SINK) mask_chunk_first(s, c, lo, hi, S - key0);
+                    else mask_chunk(s, c, lo, hi);
+                }
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
                     if ((kPolyGroups >> g) & 1u) {
@@ -370,13 +413,31 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int i = 0; i < 16; ++i) {
                     const float2 ds = f2mul(p2[16 * c + i], f2sub(raw2(dp, 2 * i), d2));
                     pk[i] = pack_bf16x2(ds.x, ds.y);
+                    if (SINK) {
+                        e2 = f2add(e2, ds);
+                        pp2 = f2fma(p2[16 * c + i], p2[16 * c + i], pp2);
+                    }
                 }
                 tc::tmem_st16(tS + 16u * c, pk);
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
             mbar_arrive(dsready);
+            if (SINK && u == n_it - 1) {
+                float* sums = reinterpret_cast<float*>(smem + OFF_SUMS);
+                sums[TILE * w + row] = e2.x + e2.y;
+                if (t < T && pp2.x + pp2.y > 0.125f) *redo = 1;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                met = true;
+                Dr += sums[row] + sums[TILE + row];
+                d2 = make_float2(Dr, Dr);
+                if (w == 0 && t < T) dbuf[(int64_t)bh * Tpad + t] = Dr;
+                if (*redo) u_end = 2 * n_it;
+                if (threadIdx.x == 0) mbar_arrive(decided);
+            }
         }
+        // a warp that gave up does not leave the others at the meeting
+        if (SINK && !met) asm volatile("bar.sync 1, 256;" ::: "memory");
         // epilogue: dq = scale * dQ -> bf16, this half's 64 channels
         if (ok && wait_bar_warp(done, 0, abort_flag)) {
             tc::fence_after_sync();
@@ -428,21 +489,32 @@ static_assert(SMEM <= 232448, "shared memory");
 // read its half of dP^T, that half holds its P^T (packed, first 32 columns) and dS^T (packed,
 // last 32 columns), so the S^T region is free as soon as it has been read: the next S^T is
 // computed while this pair's gradients are formed.
+// SINK: the first S tokens stay visible to every query. blockIdx.x past the key tiles: a segment of
+// the first tile's queries past its window (sink_parts.cuh); sums of the first S keys go to parts.
+template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS_KEY, 1)
 ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const float* __restrict__ nlse2, const float* __restrict__ dbuf,
                     __nv_bfloat16* __restrict__ dv, float* __restrict__ dk_part, int B, int T, int Tpad,
-                    int H, int HG, int W, float scale_log2, int n_qtiles) {
+                    int H, int HG, int W, float scale_log2, int n_qtiles, int S_arg, const SinkParts parts) {
     using namespace ka;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int kt = blockIdx.x, grp = blockIdx.y, b = blockIdx.z;
+    const int grp = blockIdx.y, b = blockIdx.z;
+    int kt = blockIdx.x, qt_lo = kt;  // queries t in [j, j + W - 1] see key j
+    int qt_hi = SinkParts::near_hi(kt, n_qtiles, TILE, W);  // the last query tile that sees the tile
+    int slot = 0;
+    const int S = SINK ? S_arg : 0;
+    if (SINK) {
+        const SinkWork wk = parts.work((int)blockIdx.x, n_qtiles, TILE, T, W);
+        kt = wk.tile;
+        qt_lo = wk.q_lo;
+        qt_hi = wk.q_hi;
+        slot = wk.slot;
+    }
     const int j0 = kt * TILE;
-    const int qt_lo = kt;  // queries t in [j, j + W - 1] see key j
-    const int64_t last_q = (int64_t)j0 + TILE - 1 + W - 1;  // the last query that sees the tile
-    const int qt_hi = last_q / TILE < n_qtiles - 1 ? (int)(last_q / TILE) : n_qtiles - 1;
     const int n_q = qt_hi - qt_lo + 1;  // query tiles per head
     const int h0 = grp * HG;
     const int U = HG * n_q;             // (head, query tile) pairs, head-major
@@ -625,7 +697,8 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             const int tq0 = qt * TILE + HALF * w;  // first query of this half
             const float* st = reinterpret_cast<const float*>(smem + OFF_STAT + (u % 2) * STAT_BYTES) + HALF * w;
             const bool full_tile = tq0 >= j0 + TILE - 1 && tq0 + HALF - 1 <= j0 + W - 1;
-            const int lo = key - tq0, hi_e = key + W - 1 - tq0;  // valid columns [lo, hi_e]
+            // valid columns [lo, hi_e]; every later query sees one of the first tokens
+            const int lo = key - tq0, hi_e = SINK && key < S ? TILE : key + W - 1 - tq0;
             // P^T from S^T (the unit's statistics landed with its tiles); S^T is released as soon
             // as it has been read
             if (!wait_bar_warp(sfull, (uint32_t)(u & 1), abort_flag)) { ok = false; break; }
@@ -690,7 +763,14 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     uint32_t r[32];
                     tc::tmem_ld32(tV + 32u * cb, r);
                     tc::tmem_wait_ld();
-                    if (key < T) {
+                    if (SINK && parts.nseg > 0 && key < parts.R) {
+                        float* pd = parts.dv_at(slot, (int64_t)b * H + h0 + hi, key) + HALF * w + 32 * cb;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(pd + i) =
+                                make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                            __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+                    } else if (key < T && slot == 0) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             float f[8];
@@ -708,12 +788,13 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (ok && wait_bar_warp(done, 0, abort_flag)) {
             tc::fence_after_sync();
             float* out = dk_part + (((int64_t)grp * B + b) * T + key) * HD + HALF * w;
+            if (SINK && slot > 0) out = parts.dk_at(slot, grp, b, key) + HALF * w;
 #pragma unroll
             for (int cb = 0; cb < 2; ++cb) {
                 uint32_t r[32];
                 tc::tmem_ld32(tK + 32u * cb, r);
                 tc::tmem_wait_ld();
-                if (key < T) {
+                if (key < (SINK && slot > 0 ? parts.R : T)) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4*>(out + 32 * cb + i) =
@@ -845,26 +926,65 @@ cudaError_t swska_backward_tc_launch(const SkaBackwardArgs& a, cudaStream_t stre
     if ((e = make_tmap_bf16_3d(&mdo, a.dO, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mk, a.k, HD, (uint64_t)T, (uint64_t)B, 64, TILE)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mv, a.v, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(ska_bwd_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, qa::SMEM)) !=
+    if ((e = cudaFuncSetAttribute(ska_bwd_dq_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, qa::SMEM)) !=
         cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(ska_bwd_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ka::SMEM)) !=
+    if ((e = cudaFuncSetAttribute(ska_bwd_dkdv_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ka::SMEM)) !=
         cudaSuccess)
         return e;
     const int nqt = (int)(Tpad / TILE);
     const float sl = a.scale * kLog2e;
-    ska_bwd_dq_kernel<<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM, stream>>>(
-        mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt);
+    ska_bwd_dq_kernel<false><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM, stream>>>(
+        mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, 0);
     const int G = swska_backward_tc_groups(B, H, T);
-    ska_bwd_dkdv_kernel<<<dim3((unsigned)nqt, (unsigned)G, (unsigned)B), NTHREADS_KEY, ka::SMEM, stream>>>(
+    ska_bwd_dkdv_kernel<false><<<dim3((unsigned)nqt, (unsigned)G, (unsigned)B), NTHREADS_KEY, ka::SMEM, stream>>>(
         mq, mdo, mk, mv, nlse2, dbuf, static_cast<__nv_bfloat16*>(a.dv), part, B, T, (int)Tpad, H, H / G, W,
-        sl, nqt);
+        sl, nqt, 0, SinkParts());
     const int64_t n4 = (int64_t)B * T * HD / 4;
     const int64_t want = (n4 + 255) / 256, cap = 8 * (int64_t)sm_count();
     ska_bwd_dk_reduce<<<(unsigned)(want < cap ? want : cap), 256, 0, stream>>>(
         part, static_cast<__nv_bfloat16*>(a.dk), n4, G, a.scale);
     note_launches(3);
     return cudaGetLastError();
+}
+
+cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream) {
+    const int B = a.B, H = a.H, T = a.T, W = a.W;
+    const int64_t Tpad = swska_backward_tc_tpad(T);
+    if (B > 65535) return cudaErrorInvalidConfiguration;
+    const int G = swska_backward_tc_groups(B, H, T);
+    SinkParts parts = sink_parts_plan(a, TILE, G);
+    float* nlse2 = sink_parts_bind(parts, a);
+    float* dbuf = nlse2 + (size_t)B * H * Tpad;
+    // launch 1: the row statistics from the forward's output and log-sum-exp
+    const int64_t rows = (int64_t)B * H * Tpad;
+    ska_rowstats_kernel<<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2, dbuf, T,
+        (int)Tpad, rows);
+    cudaError_t e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    CUtensorMap mq, mdo, mk, mv;
+    if ((e = make_tmap_bf16_3d(&mq, a.q, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
+    if ((e = make_tmap_bf16_3d(&mdo, a.dO, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
+    if ((e = make_tmap_bf16_3d(&mk, a.k, HD, (uint64_t)T, (uint64_t)B, 64, TILE)) != cudaSuccess) return e;
+    if ((e = make_tmap_bf16_3d(&mv, a.v, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(ska_bwd_dq_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  qa::SMEM_SINK)) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(ska_bwd_dkdv_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  ka::SMEM)) != cudaSuccess)
+        return e;
+    const int nqt = (int)(Tpad / TILE);
+    const float sl = a.scale * kLog2e;
+    ska_bwd_dq_kernel<true><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM_SINK, stream>>>(
+        mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S);
+    ska_bwd_dkdv_kernel<true><<<dim3((unsigned)(nqt + parts.n_tiles * parts.nseg), (unsigned)G, (unsigned)B),
+                                NTHREADS_KEY, ka::SMEM, stream>>>(
+        mq, mdo, mk, mv, nlse2, dbuf, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T, (int)Tpad, H, H / G, W,
+        sl, nqt, a.S, parts);
+    note_launches(3);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return sink_parts_reduce(parts, a, true, stream);
 }
 
 unsigned swska_backward_tc_take_timeout_flag() {

@@ -125,10 +125,13 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 //    V tiles in L2;
 //  - otherwise the query tile fastest, dealt out in plain stride: neighbouring query tiles of
 //    a head pair run side by side whatever HP x B is, and over many rounds the loads even out.
+// With the first S tokens visible to every query, the key tiles that hold them come first, as far
+// as they lie before the window's first tile.
 struct Item {
-    int t0, kt_lo, n_it, hp, b;
+    int t0, kt_lo, n_it, hp, b, n_sink;
+    __device__ __forceinline__ int key0(int j) const { return (j < n_sink ? j : kt_lo + j - n_sink) * BN; }
 };
-__device__ __forceinline__ Item item_at(int i, int n_qtiles, int HP, int NHB, int W, bool qt_slow) {
+__device__ __forceinline__ Item item_at(int i, int n_qtiles, int HP, int NHB, int W, bool qt_slow, int S = 0) {
     Item it;
     int qt, rest;
     if (qt_slow) {
@@ -142,7 +145,8 @@ __device__ __forceinline__ Item item_at(int i, int n_qtiles, int HP, int NHB, in
     it.b = rest / HP;
     it.t0 = qt * BM;
     it.kt_lo = (it.t0 - W + 1 > 0 ? it.t0 - W + 1 : 0) / BN;
-    it.n_it = it.t0 / BN - it.kt_lo + 1;
+    it.n_sink = min((S + BN - 1) / BN, it.kt_lo);
+    it.n_it = it.t0 / BN - it.kt_lo + 1 + it.n_sink;
     return it;
 }
 // the k-th item of this CTA (round k of gridDim.x items), or -1 past the last
@@ -154,14 +158,17 @@ __device__ __forceinline__ int cta_item(int k, int n_items, bool snake) {
 }
 
 // STATS: the statistics mode (each row's log-sum-exp times lse_mul, D = dO . o when dO is given,
-// output optional); a separate instantiation so the plain forward carries none of its registers
-template <bool STATS, bool QT_SLOW>
+// output optional); a separate instantiation so the plain forward carries none of its registers.
+// SINK: the first S tokens stay visible to every query (S = 0 otherwise): up to one more key tile per
+// item, and on the masked tiles a third comparison per score
+template <bool STATS, bool QT_SLOW, bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, __nv_bfloat16* __restrict__ o, int T,
                 int H, int W, float scale_log2, int n_qtiles, int n_items,
                 const __nv_bfloat16* __restrict__ dO,
-                float* __restrict__ lse, float* __restrict__ dbuf, int Tpad, float lse_mul) {
+                float* __restrict__ lse, float* __restrict__ dbuf, int Tpad, float lse_mul, int S_arg) {
+    const int S = SINK ? S_arg : 0;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -223,7 +230,7 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int k_item = 0; ok; ++k_item) {
                 const int item = cta_item(k_item, n_items, QT_SLOW);
                 if (item < 0) break;
-                const Item it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW);
+                const Item it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW, S);
                 // the previous item's last S has read its Q
                 if (nq > 0 && !wait_bar(qempty, (uint32_t)((nq - 1) & 1), abort_flag)) break;
                 mbar_arrive_expect_tx(qfull, 2 * TILE_BYTES);
@@ -239,7 +246,7 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         ok = false;
                         break;
                     }
-                    const int j = l / 3, which = l % 3, key0 = (it.kt_lo + j) * BN;
+                    const int j = l / 3, which = l % 3, key0 = it.key0(j);
                     unsigned char* dst = smem + OFF_RING + slot * TILE_BYTES;
                     mbar_arrive_expect_tx(&full[slot], TILE_BYTES);
                     for (int half = 0; half < 2; ++half) {
@@ -310,7 +317,7 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         for (int k_item = 0; ok; ++k_item) {
             const int item = cta_item(k_item, n_items, QT_SLOW);
             if (item < 0) break;
-            const int n_it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW).n_it;
+            const int n_it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW, S).n_it;
             if (!handoff(qfull, items) || !acquire(Lb)) break;
             issue_s(0, Lb);
             tc::mma_commit_warp(&sfull[0]);
@@ -375,8 +382,8 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         for (int k_item = 0; ok; ++k_item) {
             const int item = cta_item(k_item, n_items, QT_SLOW);
             if (item < 0) break;
-            const Item it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW);
-            const int t0 = it.t0, kt_lo = it.kt_lo, n_it = it.n_it, hp = it.hp, b = it.b;
+            const Item it = item_at(item, n_qtiles, HP, NHB, W, QT_SLOW, S);
+            const int t0 = it.t0, n_it = it.n_it, hp = it.hp, b = it.b;
             const int t = t0 + row;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < n_it; ++j) {
@@ -388,13 +395,14 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tc::tmem_ld32(tS + 64, s + 64);
                 tc::tmem_ld32(tS + 96, s + 96);
                 tc::tmem_wait_ld();
-                const int key0 = (kt_lo + j) * BN;
-                const bool full_tile = key0 >= t0 + BM - W && key0 + BN - 1 <= t0;
+                const int key0 = it.key0(j);
+                const bool full_tile = (key0 >= t0 + BM - W || (SINK && key0 + BN <= S)) && key0 + BN - 1 <= t0;
                 if (!full_tile) {
-                    const int lo = t - W + 1 - key0, hi = t - key0;  // valid key columns [lo, hi]
+                    const int lo = t - W + 1 - key0, hi = t - key0;  // valid key columns [lo, hi], and
+                    const int first = S - key0;                      // those before `first`
 #pragma unroll
                     for (int c = 0; c < BN; ++c)
-                        if (c < lo || c > hi) s[c] = 0xff800000u;  // -inf
+                        if ((c < lo && (!SINK || c >= first)) || c > hi) s[c] = 0xff800000u;  // -inf
                 }
                 // row maximum: 8 independent chains of 3-input maxima over the columns c = 8k + i
                 float m8[8];
@@ -536,7 +544,7 @@ cudaError_t swska_prefill_tc_launch(const void* q, const void* k, const void* v,
 cudaError_t swska_prefill_tc_stats_launch(const void* q, const void* k, const void* v, void* o,
                                           const void* dO, float* lse, float* dbuf, int64_t Tpad, int B,
                                           int H, int T, int window, float scale, cudaStream_t stream,
-                                          float lse_mul) {
+                                          float lse_mul, int sinks) {
     CUtensorMap mq, mk, mv;
     cudaError_t e;
     if ((e = make_tmap_bf16_3d(&mq, q, HD, (uint64_t)T, (uint64_t)B * H, 64, BM)) != cudaSuccess) return e;
@@ -555,13 +563,14 @@ cudaError_t swska_prefill_tc_stats_launch(const void* q, const void* k, const vo
     const int sms = sm_count();
     const unsigned grid = (unsigned)(n_items < sms ? n_items : sms);
     const bool qt_slow = (int64_t)((H + 1) / 2) * B <= 32 && n_items < 16 * (int64_t)sms;
-    auto* kern = stats ? (qt_slow ? swska_tc_kernel<true, true> : swska_tc_kernel<true, false>)
-                       : (qt_slow ? swska_tc_kernel<false, true> : swska_tc_kernel<false, false>);
+    auto* kern = stats ? (qt_slow ? swska_tc_kernel<true, true, false> : swska_tc_kernel<true, false, false>)
+                       : (qt_slow ? swska_tc_kernel<false, true, false> : swska_tc_kernel<false, false, false>);
+    if (sinks > 0) kern = qt_slow ? swska_tc_kernel<true, true, true> : swska_tc_kernel<true, false, true>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) != cudaSuccess)
         return e;
     kern<<<grid, NTHREADS, SMEM_BYTES, stream>>>(
         mq, mk, mv, static_cast<__nv_bfloat16*>(o), T, H, window, scale * 1.4426950408889634f,
-        n_qtiles, (int)n_items, static_cast<const __nv_bfloat16*>(dO), lse, dbuf, (int)Tpad, lse_mul);
+        n_qtiles, (int)n_items, static_cast<const __nv_bfloat16*>(dO), lse, dbuf, (int)Tpad, lse_mul, sinks);
     note_launches(1);
     return cudaGetLastError();
 }

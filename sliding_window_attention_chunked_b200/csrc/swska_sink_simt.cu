@@ -104,12 +104,16 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
 template <int DK, int DV>
 constexpr int dq_smem() { return (BQ * (ld<DK>() + ld<DV>()) + BK * (ld<DK>() + ld<DV>()) + BQ * LDP) * 4; }
 
-template <int DK, int DV>
+// With bf16 rows D from the stored o is off by about 2^-9 of it, which a row whose attention is peaked
+// turns into a larger error of dS = p (dP - D): there D0 from o only centres the sums, and
+//   e = sum_j p_j (dP_j - D0),  dq = scale (sum_j p_j (dP_j - D0) k_j - e sum_j p_j k_j),  D = D0 + e
+// gives the row's own D in the same pass, for one more product per tile.
+template <int DK, int DV, bool BF16>
 __global__ void __launch_bounds__(NTH)
 sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                const void* __restrict__ o, const float* __restrict__ lse, const void* __restrict__ dO,
-               void* __restrict__ dq, float* __restrict__ dbuf, bool bf16, int H, int T, int W, int S, float scale,
-               int qtiles) {
+               void* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
+    constexpr bool bf16 = BF16;
     extern __shared__ __align__(16) float sm[];
     float* sQ = sm;
     float* sG = sQ + BQ * ld<DK>();
@@ -124,10 +128,11 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
     load_tile<DK, BQ, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
     load_tile<DV, BQ, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
     __syncthreads();
-    float L2[4], D[4], acc[4][DK / 16];
+    float L2[4], D[4], e[4], acc[4][DK / 16], pk[4][BF16 ? DK / 16 : 1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, t = t0 + r;
+        e[i] = 0.f;
         float d = 0.f;
         if (t < T)
             for (int c = tx; c < DV; c += 16) {
@@ -137,9 +142,12 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
             }
         D[i] = row_sum(d);
         L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
-        if (tx == 0 && t < T) dbuf[bh * T + t] = D[i];
+        if (!BF16 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
 #pragma unroll
-        for (int c = 0; c < DK / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < DK / 16; ++c) {
+            acc[i][c] = 0.f;
+            if (BF16) pk[i][c] = 0.f;
+        }
     }
     const KeyTiles kt = key_tiles(t0, t1, W, S);
     for (int it = 0; it < kt.n; ++it) {
@@ -156,15 +164,29 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool see = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S);
-                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) * (g[i][j] - D[i]) : 0.f;
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) : 0.f;
+                g[i][j] = s[i][j] * (g[i][j] - D[i]);
+                e[i] += g[i][j];
             }
-        put_tile(sP, ty, tx, s);
+        put_tile(sP, ty, tx, g);
         __syncthreads();
         tile_mul<DK>(sP, sK, ty, tx, acc);
+        if constexpr (BF16) {
+            __syncthreads();
+            put_tile(sP, ty, tx, s);
+            __syncthreads();
+            tile_mul<DK>(sP, sK, ty, tx, pk);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + 4 * ty + i;
+        if constexpr (BF16) {
+            const float er = row_sum(e[i]);
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c) acc[i][c] = fmaf(-er, pk[i][c], acc[i][c]);
+            if (tx == 0 && t < T) dbuf[bh * T + t] = D[i] + er;
+        }
         if (t >= T) continue;
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c)
@@ -280,14 +302,15 @@ cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
     SinkParts parts = sink_parts_plan(a, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(sink_dq_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, true> : sink_dq_kernel<DK, DV, false>;
+    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   dq_smem<DK, DV>())) != cudaSuccess)
         return e;
     if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   dkv_smem<DK, DV>())) != cudaSuccess)
         return e;
-    sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH, dq_smem<DK, DV>(), s>>>(
-        a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, bf16, a.H, a.T, a.W, a.S, a.scale, tiles);
+    dq_kernel<<<(unsigned)grid, NTH, dq_smem<DK, DV>(), s>>>(
+        a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W, a.S, a.scale, tiles);
     sink_dkv_kernel<DK, DV><<<dim3((unsigned)(tiles + parts.n_tiles * parts.nseg), (unsigned)a.H, (unsigned)a.B), NTH,
                               dkv_smem<DK, DV>(), s>>>(a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H,
                                                        a.T, a.W, a.S, a.scale, tiles);
@@ -322,16 +345,23 @@ cudaError_t pick(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
 cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, false, s); }
 cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, true, s); }
 
+// bf16 with 128-wide heads and at least one full tile runs on the tensor cores
 cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    if (bf16 && swska_prefill_tc_supported(a.H, a.T, a.d_k, a.d_v))
+        return swska_prefill_tc_stats_launch(a.q, a.k, a.v, a.out, nullptr, a.lse_out, nullptr, a.T, a.B, a.H, a.T, a.W,
+                                             a.scale, s, kLn2, a.S);
     return swska_sink_prefill_simt_launch(a, bf16, s);
 }
 cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    if (bf16 && swska_backward_tc_supported(a.H, a.T, a.d_k, a.d_v)) return swska_sink_backward_tc_launch(a, s);
     return swska_sink_backward_simt_launch(a, bf16, s);
 }
 size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S) {
     SinkArgs a{};
     a.B = B, a.H = H, a.T = T, a.d_k = dk, a.d_v = dv, a.W = W, a.S = S;
-    return sink_parts_floats(sink_parts_plan(a, BK, H)) * sizeof(float);
+    // enough for either route: tiles of 64 or 128 keys, at most H head groups
+    const size_t x = sink_parts_floats(sink_parts_plan(a, BK, H)), y = sink_parts_floats(sink_parts_plan(a, 128, H));
+    return (x > y ? x : y) * sizeof(float);
 }
 
 }  // namespace rod
