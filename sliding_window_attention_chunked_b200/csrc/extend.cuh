@@ -15,26 +15,38 @@
 
 namespace rod {
 
-struct ExtendUnit {  // 32 bytes
+struct ExtendUnit {  // 48 bytes: all that a CTA needs besides the table, so that it waits for one load
     int n, q0;       // sequence, its first query of the tile
     int kt0, kt1;    // this unit's range in the tile's list of key tiles
     int part;        // first part of the tile (parts are numbered like units), -1: not split
     int nsplit;
     int split;
     int item;        // the tile's counter row
+    int row0, len, ctx, pad;  // of the sequence (ExtendSeq)
 };
 
 struct ExtendRoute {
     int rows = 0, tile = 0;  // queries per tile (0: route not used), keys per key tile
     int groups = 1;          // head groups: CTAs per unit
-    int target = 1;          // units x groups to reach by splitting
+    int target = 1;          // units x groups to reach by splitting, in units of at least
+    int share = 1;           // min(min_tiles, all tiles / share) key tiles
+    int min_tiles = 1;
+    int part_rows = 0;       // rows kept of a part
     int cap_units = 0, cap_items = 0, cap_parts = 0;
     ExtendUnit* units = nullptr;
     int* n_units = nullptr;
     int* count = nullptr;    // [cap_items_split][H]
-    float* part_o = nullptr; // [cap_parts][H][rows][dv]
-    float2* part_ml = nullptr;  // [cap_parts][H][rows]
+    float* part_o = nullptr; // [cap_parts][H][part_rows][dv]
+    float2* part_ml = nullptr;  // [cap_parts][H][part_rows]: maximum (base 2) and sum
+    __device__ __forceinline__ int64_t part_at(int unit, int H, int h, int row) const {
+        return ((int64_t)unit * H + h) * part_rows + row;
+    }
 };
+__device__ __forceinline__ ExtendUnit load_unit(const ExtendUnit* p) {
+    const int4* x = reinterpret_cast<const int4*>(p);
+    const int4 a = __ldcg(x), b = __ldcg(x + 1), c = __ldcg(x + 2);
+    return ExtendUnit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+}
 
 struct ExtendPlan {
     ExtendRoute r[2];  // [0] sequences of at most short_len new tokens, [1] the others
@@ -88,7 +100,15 @@ __device__ __forceinline__ int extend_page(const ExtendArgs& a, int n, int page)
 ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf16);
 size_t extend_bind(ExtendPlan& p, int H, int dv, void* workspace);  // returns the bytes
 
+// The launch before wrote the units and the cache: a kernel launched to overlap its tail waits here.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // kernels; each launcher runs one route of the plan
 cudaError_t swska_extend_simt_launch(const ExtendArgs& a, const ExtendRoute& r, bool bf16, cudaStream_t s);
+cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, cudaStream_t s);
+unsigned swska_extend_few_take_timeout_flag();
+constexpr int kFewRows = 16;   // bf16, 128-wide heads: sequences of at most this many new tokens
+constexpr int kFewTile = 32;   // keys per tile there
+constexpr int kFewHeads = 8;   // heads per CTA there
 
 }  // namespace rod

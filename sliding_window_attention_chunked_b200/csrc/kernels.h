@@ -182,5 +182,6 @@ struct ExtendArgs {
 };
 size_t swska_extend_workspace_size(int M, int N, int H, int dk, int dv, int max_len, bool bf16);
 cudaError_t swska_extend_launch(const ExtendArgs& a, bool bf16, cudaStream_t s);
+unsigned swska_extend_take_timeout_flag();
 
 }  // namespace rod

@@ -77,7 +77,8 @@ int rod_check(void* stream) {
                            rod::swska_prefill_tc_take_timeout_flag() |
                            rod::gla_prefill_tc_take_timeout_flag() |
                            rod::gla_backward_tc_take_timeout_flag() |
-                           rod::swska_backward_tc_take_timeout_flag();
+                           rod::swska_backward_tc_take_timeout_flag() |
+                           rod::swska_extend_take_timeout_flag();
     if (flags) return ROD_ERR_TIMEOUT;
     return from_cuda(cudaGetLastError());
 }

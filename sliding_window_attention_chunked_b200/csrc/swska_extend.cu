@@ -56,6 +56,8 @@ __device__ __forceinline__ SeqWork seq_work(const ExtendArgs& a, const ExtendPla
 }
 
 __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, const ExtendPlan p) {
+    // the attention kernel may set itself up meanwhile; it waits for this launch's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x > 0) {
         // ---- new keys and values to their slots, 16 bytes a thread
         if (a.k_new == nullptr) return;
@@ -117,6 +119,9 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
         long long C = 1ll << 40;
         if ((long long)n_items * r.groups < r.target) {
             C = (n_tiles * r.groups + r.target - 1) / r.target;
+            const long long even = (n_tiles * r.groups + r.share - 1) / r.share;
+            const long long least = even < r.min_tiles ? even : r.min_tiles;
+            if (C < least) C = least;
             if (C < 1) C = 1;
             for (int x = threadIdx.x; x < n_items * a.H; x += NT) r.count[x] = 0;
         }
@@ -150,13 +155,18 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
                 e.item = s_items[l] + local / nsp;
                 const int at_u = units + u;
                 e.part = nsp > 1 ? at_u - e.split : -1;
-                const ExtendKeys k = extend_keys(extend_seq(a, e.n), e.q0, r.rows, r.tile, a.W, a.S);
+                const ExtendSeq sq = extend_seq(a, e.n);
+                e.row0 = sq.row0;
+                e.len = sq.len;
+                e.ctx = sq.ctx;
+                const ExtendKeys k = extend_keys(sq, e.q0, r.rows, r.tile, a.W, a.S);
                 e.kt0 = (int)((long long)e.split * k.n / nsp);
                 e.kt1 = (int)((long long)(e.split + 1) * k.n / nsp);
                 if (at_u < r.cap_units) {
                     int4* to = reinterpret_cast<int4*>(r.units + at_u);
                     to[0] = make_int4(e.n, e.q0, e.kt0, e.kt1);
                     to[1] = make_int4(e.part, e.nsplit, e.split, e.item);
+                    to[2] = make_int4(e.row0, e.len, e.ctx, 0);
                 }
             }
             units += tot_u;
@@ -174,24 +184,35 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf16) {
     ExtendPlan p;
     if (max_len > M) max_len = M;
-    auto route = [&](int i, int rows, int tile, int groups, int target, int items) {
+    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int target, int share, int min_tiles,
+                     int64_t items) {
         ExtendRoute& r = p.r[i];
         r.rows = rows;
         r.tile = tile;
         r.groups = groups;
+        r.part_rows = part_rows;
         r.target = target;
-        r.cap_items = items;
+        r.share = share;
+        r.min_tiles = min_tiles;
+        r.cap_items = (int)items;
         // split units: at most one per query tile and target / groups more (sum of ceil(t / C))
         const int split = 2 * (target / groups + 1);
-        r.cap_units = items > split ? items : split;
+        r.cap_units = items > split ? (int)items : split;
         r.cap_parts = split;
     };
     const int sms = device_sm_count();
+    if (bf16 && dk == 128 && dv == 128 && max_len <= kFewRows) {
+        // One CTA per SM. Units of equal length come in whole rounds, so a few rounds waste part of the
+        // last one; more, shorter units waste less and add parts of at most max_len rows per head.
+        const int few = max_len < kFewRows ? max_len : kFewRows;
+        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, few <= 4 ? 8 * sms : 2 * sms, sms, 8, N);
+        return p;
+    }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
     const int rows = max_len <= 16 ? 16 : 64;
     int64_t items = (int64_t)M / rows + N;
     if (items > M) items = M;
-    route(0, rows, 64, H, 4 * sms, (int)items);
+    route(0, rows, rows, 64, H, 4 * sms, sms, 1, items);
     return p;
 }
 
@@ -210,8 +231,8 @@ size_t extend_bind(ExtendPlan& p, int H, int dv, void* workspace) {
         r.units = reinterpret_cast<ExtendUnit*>(take((size_t)r.cap_units * sizeof(ExtendUnit)));
         // counters exist for split tiles only, and those are fewer than target / groups
         r.count = reinterpret_cast<int*>(take((size_t)r.cap_parts * H * sizeof(int)));
-        r.part_ml = reinterpret_cast<float2*>(take((size_t)r.cap_parts * H * r.rows * sizeof(float2)));
-        r.part_o = reinterpret_cast<float*>(take((size_t)r.cap_parts * H * r.rows * dv * sizeof(float)));
+        r.part_ml = reinterpret_cast<float2*>(take((size_t)r.cap_parts * H * r.part_rows * sizeof(float2)));
+        r.part_o = reinterpret_cast<float*>(take((size_t)r.cap_parts * H * r.part_rows * dv * sizeof(float)));
     }
     return at;
 }
@@ -230,7 +251,10 @@ cudaError_t swska_extend_launch(const ExtendArgs& a, bool bf16, cudaStream_t s) 
     note_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (p.r[0].tile == kFewTile) return swska_extend_few_launch(a, p.r[0], s);
     return swska_extend_simt_launch(a, p.r[0], bf16, s);
 }
+
+unsigned swska_extend_take_timeout_flag() { return swska_extend_few_take_timeout_flag(); }
 
 }  // namespace rod

@@ -1,0 +1,386 @@
+// swska_extend_few.cu -- SW-SKA attention of a few new tokens (at most 16 per sequence: decode steps,
+// speculative tokens) over a paged cache, bf16, 128-wide heads.
+//
+//   o[i,h] = sum_j softmax_j(scale q[i,h] . k[j]) v[h,j],  j <= p, j > p - W or j < S,  p = ctx + i
+// Few queries against a window of keys: every value row is used for at most 16 dot products, so the
+// kernel is bound by reading the cache (values: H times the keys) from HBM. A CTA takes a unit (one
+// sequence, some key tiles of 32) of up to eight heads, so that the shared key tile is fetched once
+// for them: one warp per head, which multiplies with m16n8k16 instructions (16 query rows; a
+// tcgen05 tile of 128 rows would be seven eighths padding), and one warp that feeds a ring of
+// stages of a key tile and eight value tiles by TMA, 72 KB a stage: three stages hold more than the
+// bytes in flight that HBM's rate times its latency asks of an SM. The pages' rows land in shared
+// memory with the 128-byte swizzle, which keeps the fragment loads free of bank conflicts; a page of
+// any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows.
+// Softmax: running maximum and sum in fp32, base 2; the output is rescaled only when a row's maximum
+// moves. Probabilities go to the second product in bf16 (relative 2^-9 each, like the cached values).
+#include <cuda.h>
+#include <math.h>
+
+#include "extend.cuh"
+#include "tc.cuh"
+
+namespace rod {
+namespace {
+
+__device__ unsigned int g_extend_few_timeout = 0;
+
+constexpr int HD = 128;
+constexpr int KT = kFewTile;               // keys per tile
+constexpr int HALF = KT * 128;             // bytes: KT rows x 64 columns
+constexpr int TILE = 2 * HALF;             // 8 KB: a key tile or one head's value tile
+constexpr int NTH = 32 * (kFewHeads + 1);
+constexpr int MAXST = 12;
+constexpr int RING = 216 * 1024;
+constexpr int OFF_BAR = RING;
+constexpr int OFF_MASK = OFF_BAR + 2 * MAXST * 8;
+constexpr int OFF_MISC = OFF_MASK + MAXST * 4;
+constexpr int SMEM = OFF_MISC + 16 + 1024;
+static_assert(SMEM <= 232448, "shared memory");
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 255u) == 0) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            if (i >= kWaitLimit) {
+                *abort_flag = 1;
+                atomicExch(&g_extend_few_timeout, 1u);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// 16-byte chunk c (of 16) of row r of a tile: two halves of 64 columns, swizzled
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)((c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__global__ void __launch_bounds__(NTH, 1)
+extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const ExtendArgs a, const ExtendRoute r, int hpg, int n_stages, int box, float scale_log2) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* empty = full + MAXST;
+    volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + OFF_MASK);  // keys whose page exists
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC);
+    const int stage_bytes = TILE * (1 + hpg);
+
+    // a CTA keeps to one head group: blockIdx.x = group + groups * column
+    const int grp = blockIdx.x % r.groups, cols = gridDim.x / r.groups;
+    const int h0 = grp * hpg, nh = min(hpg, a.H - h0);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < n_stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], (uint32_t)nh);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    wait_for_launch_before();
+    const int n_units = __ldcg(r.n_units);
+
+    if (warp == kFewHeads) {
+        // ------------------------------- producer -------------------------------
+        if (lane == 0) {
+            tc::tma_prefetch_desc(&tm_k);
+            tc::tma_prefetch_desc(&tm_v);
+        }
+        const int nbox = KT / box, ops = 2 * nbox * (1 + nh);
+        int t = 0;  // tiles fed so far
+        bool ok = true;
+        for (int x = blockIdx.x / r.groups; x < n_units && ok; x += cols) {
+            const ExtendUnit u = load_unit(r.units + x);
+            const ExtendSeq sq{u.row0, u.len, u.ctx, false};
+            const ExtendKeys kt = extend_keys(sq, u.q0, kFewRows, KT, a.W, a.S);
+            // lanes 0 .. nbox - 1 hold the page of the tile's box, one tile ahead
+            auto page_of = [&](int i) {
+                return i < u.kt1 && lane < nbox ? extend_page(a, u.n, (kt.at(i) * KT + lane * box) / a.page) : -1;
+            };
+            int pg_next = page_of(u.kt0);
+            for (int i = u.kt0; i < u.kt1; ++i, ++t) {
+                const int pg = pg_next, key0 = kt.at(i) * KT;
+                pg_next = page_of(i + 1);
+                const int s = t % n_stages, use = t / n_stages;
+                if (use > 0 && !wait_warp(&empty[s], (uint32_t)((use - 1) & 1), abort_flag)) { ok = false; break; }
+                unsigned have = 0;
+                for (int b = 0; b < nbox; ++b)
+                    if (__shfl_sync(0xffffffffu, pg, b) >= 0) have |= (box == 32 ? 0xffffffffu : ((1u << box) - 1u) << (b * box));
+                if (lane == 0) {
+                    mask[s] = have;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)(TILE * (1 + nh)));
+                }
+                __syncwarp();
+                for (int o0 = 0; o0 < ops; o0 += 32) {
+                    const int op = o0 + lane;
+                    const int b = op % nbox, half = op / nbox % 2, which = op / (2 * nbox);  // 0: keys, 1 + h: values
+                    const int p = __shfl_sync(0xffffffffu, pg, b);
+                    if (op < ops) {
+                        unsigned char* dst = smem + s * stage_bytes + which * TILE + half * HALF + b * box * 128;
+                        const int y = (key0 + b * box) % a.page;
+                        // a page that the table does not have: a coordinate past the end, which fills zeros
+                        if (which == 0) tc::tma_load_3d(dst, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[s]);
+                        else tc::tma_load_3d(dst, &tm_v, half * 64, y, p >= 0 ? p * a.H + h0 + which - 1 : a.P * a.H, &full[s]);
+                    }
+                }
+            }
+        }
+        // every copy started here has landed before the CTA can leave
+        for (int i = t > n_stages ? t - n_stages : 0; i < t; ++i)
+            mbar_wait_bounded(&full[i % n_stages], (uint32_t)((i / n_stages) & 1), kWaitLimit);
+        return;
+    }
+    if (warp >= nh) return;
+    // ------------------------------- one warp per head -------------------------------
+    const int h = h0 + warp;
+    const int g = lane / 4, c2 = 2 * (lane % 4);  // this thread's rows g, g + 8 and its column pair
+    const int mat = lane / 8, mr = lane % 8;      // this lane's row address in a 4-matrix load
+    int t = 0;
+    for (int x = blockIdx.x / r.groups; x < n_units; x += cols) {
+        const ExtendUnit u = load_unit(r.units + x);
+        const ExtendSeq sq{u.row0, u.len, u.ctx, false};
+        const ExtendKeys kt = extend_keys(sq, u.q0, kFewRows, KT, a.W, a.S);
+        const int rows = min(u.len - u.q0, kFewRows), p0 = u.ctx + u.q0, p1 = p0 + rows - 1;
+        const int64_t row0 = u.row0 + u.q0;
+        uint32_t qa[8][4];
+        {
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+            const uint32_t* q0p = reinterpret_cast<const uint32_t*>(q + ((row0 + g) * a.H + h) * HD + c2);
+            const uint32_t* q1p = reinterpret_cast<const uint32_t*>(q + ((row0 + g + 8) * a.H + h) * HD + c2);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                qa[k][0] = g < rows ? q0p[8 * k] : 0u;
+                qa[k][1] = g + 8 < rows ? q1p[8 * k] : 0u;
+                qa[k][2] = g < rows ? q0p[8 * k + 4] : 0u;
+                qa[k][3] = g + 8 < rows ? q1p[8 * k + 4] : 0u;
+            }
+        }
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int i = u.kt0; i < u.kt1; ++i, ++t) {
+            const int st = t % n_stages, key0 = kt.at(i) * KT;
+            if (!wait_warp(&full[st], (uint32_t)((t / n_stages) & 1), abort_flag)) return;
+            const uint32_t kb = smem_u32(smem + st * stage_bytes), vb = kb + (1 + warp) * TILE;
+            float s[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+                    uint32_t b[4];
+                    ldsm4(kb + chunk_at((n + (mat >> 1)) * 8 + mr, 2 * k + (mat & 1)), b);
+                    mma16816(s[n], qa[k], b);
+                    mma16816(s[n + 1], qa[k], b + 2);
+                }
+            const uint32_t have = mask[st];
+            const bool whole = have == 0xffffffffu && key0 + KT - 1 <= p0 &&
+                               ((int64_t)key0 > (int64_t)p1 - a.W || key0 + KT <= a.S);
+            bool zeroed = false;
+            if (!whole) {
+                // keys that no query sees: the rows behind them may hold anything, so clear this head's
+                const int j = key0 + lane;
+                const bool seen = (have >> lane & 1u) && j <= p1 && ((int64_t)j > (int64_t)p0 - a.W || j < a.S);
+                unsigned drop = ~__ballot_sync(0xffffffffu, seen);
+                zeroed = drop != 0;
+                while (drop) {
+                    const int key = __ffs(drop) - 1;
+                    drop &= drop - 1;
+                    if (lane < 16)
+                        *reinterpret_cast<uint4*>(smem + st * stage_bytes + (1 + warp) * TILE + chunk_at(key, lane)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 8 * n + c2 + (e & 1), key = key0 + c, p = p0 + g + (e & 2) * 4;
+                        const bool see = (have >> c & 1u) && key <= p && ((int64_t)key > (int64_t)p - a.W || key < a.S);
+                        if (!see) s[n][e] = -INFINITY;
+                    }
+            }
+            // row maxima over the four threads of a row
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                mx[0] = fmaxf(mx[0], fmaxf(s[n][0], s[n][1]));
+                mx[1] = fmaxf(mx[1], fmaxf(s[n][2], s[n][3]));
+            }
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
+            }
+            const float t0 = mx[0] * scale_log2, t1 = mx[1] * scale_log2;
+            if (__any_sync(0xffffffffu, t0 > m[0] || t1 > m[1])) {
+                const float n0 = fmaxf(m[0], t0), n1 = fmaxf(m[1], t1);
+                const float a0 = n0 == -INFINITY ? 1.f : tc::ex2(m[0] - n0), a1 = n1 == -INFINITY ? 1.f : tc::ex2(m[1] - n1);
+                m[0] = n0;
+                m[1] = n1;
+                l[0] *= a0;
+                l[1] *= a1;
+#pragma unroll
+                for (int i2 = 0; i2 < 16; ++i2) {
+                    o[i2][0] *= a0;
+                    o[i2][1] *= a0;
+                    o[i2][2] *= a1;
+                    o[i2][3] *= a1;
+                }
+            }
+            const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                s[n][0] = tc::ex2(fmaf(s[n][0], scale_log2, -b0));
+                s[n][1] = tc::ex2(fmaf(s[n][1], scale_log2, -b0));
+                s[n][2] = tc::ex2(fmaf(s[n][2], scale_log2, -b1));
+                s[n][3] = tc::ex2(fmaf(s[n][3], scale_log2, -b1));
+                l[0] += s[n][0] + s[n][1];
+                l[1] += s[n][2] + s[n][3];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t pa[4];
+                pa[0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
+                pa[1] = pack_bf16x2(s[2 * k][2], s[2 * k][3]);
+                pa[2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
+                pa[3] = pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]);
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    uint32_t b[4];
+                    ldsm4t(vb + chunk_at(16 * k + (mat & 1) * 8 + mr, c + (mat >> 1)), b);
+                    mma16816(o[c], pa, b);
+                    mma16816(o[c + 1], pa, b + 2);
+                }
+            }
+            if (zeroed) tc::fence_proxy_async();  // before the next copy into this stage
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+            l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+        }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
+        if (u.part < 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = g + 8 * e;
+                if (row >= rows) continue;
+                const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+                __nv_bfloat16* op = out + ((row0 + row) * a.H + h) * HD + c2;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    *reinterpret_cast<uint32_t*>(op + 8 * c) = pack_bf16x2(o[c][2 * e] * inv, o[c][2 * e + 1] * inv);
+            }
+            continue;
+        }
+        // this unit's part; the warp that comes last for the head adds the parts in the order of the keys
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = g + 8 * e;
+            if (row >= rows) continue;
+            const int64_t at = r.part_at(u.part + u.split, a.H, h, row);
+            if (lane % 4 == 0) r.part_ml[at] = make_float2(m[e], l[e]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                *reinterpret_cast<float2*>(r.part_o + at * HD + 8 * c + c2) = make_float2(o[c][2 * e], o[c][2 * e + 1]);
+        }
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = atomicAdd(r.count + (int64_t)u.item * a.H + h, 1) == u.nsplit - 1;
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        __threadfence();
+        for (int row = 0; row < rows; ++row) {
+            float M = -INFINITY;
+            for (int s = lane; s < u.nsplit; s += 32)
+                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part + s, a.H, h, row)].x));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            const float base = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int s = 0; s < u.nsplit; ++s) {
+                const int64_t at = r.part_at(u.part + s, a.H, h, row);
+                const float2 ml = __ldcg(&r.part_ml[at]);
+                const float4 x4 = __ldcg(reinterpret_cast<const float4*>(r.part_o + at * HD) + lane);
+                const float w = tc::ex2(ml.x - base);
+                L = fmaf(ml.y, w, L);
+                O.x = fmaf(x4.x, w, O.x);
+                O.y = fmaf(x4.y, w, O.y);
+                O.z = fmaf(x4.z, w, O.z);
+                O.w = fmaf(x4.w, w, O.w);
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            store4(out + ((row0 + row) * a.H + h) * HD + 4 * lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, cudaStream_t s) {
+    const int hpg = (a.H + r.groups - 1) / r.groups;
+    int box = KT;
+    while (a.page % box != 0) box /= 2;
+    CUtensorMap mk, mv;
+    cudaError_t e;
+    if ((e = make_tmap_bf16_3d(&mk, a.k_pool, HD, (uint64_t)a.page, (uint64_t)a.P, 64, (uint32_t)box)) != cudaSuccess) return e;
+    if ((e = make_tmap_bf16_3d(&mv, a.v_pool, HD, (uint64_t)a.page, (uint64_t)a.P * a.H, 64, (uint32_t)box)) != cudaSuccess) return e;
+    int stages = RING / (TILE * (1 + hpg));
+    if (stages > MAXST) stages = MAXST;
+    if ((e = cudaFuncSetAttribute(extend_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
+    // every column of CTAs covers all head groups; one CTA per SM
+    const int64_t want = r.cap_units;
+    int64_t cols = device_sm_count() / r.groups;
+    if (cols < 1) cols = 1;
+    if (cols > want) cols = want;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(cols * r.groups));
+    cfg.blockDim = dim3(NTH);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, extend_few_kernel, mk, mv, a, r, hpg, stages, box, a.scale * 1.4426950408889634f);
+    note_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+unsigned swska_extend_few_take_timeout_flag() {
+    unsigned v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_extend_few_timeout, sizeof(v)) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(g_extend_few_timeout, &zero, sizeof(zero));
+    return v;
+}
+
+}  // namespace rod

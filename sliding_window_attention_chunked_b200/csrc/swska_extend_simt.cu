@@ -36,9 +36,9 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     const int n_work = *r.n_units * a.H;
     for (int x = blockIdx.x; x < n_work; x += gridDim.x) {
-        const ExtendUnit u = r.units[x / a.H];
+        const ExtendUnit u = load_unit(r.units + x / a.H);
         const int h = x % a.H;
-        const ExtendSeq sq = extend_seq(a, u.n);
+        const ExtendSeq sq{u.row0, u.len, u.ctx, false};
         const int rows = sq.len - u.q0 < BQ ? sq.len - u.q0 : BQ;
         const int p0 = sq.ctx + u.q0, p1 = p0 + rows - 1;
         const ExtendKeys kt = extend_keys(sq, u.q0, BQ, BK, a.W, a.S);
@@ -97,7 +97,7 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
             continue;
         }
         // this unit's part, then the last unit of the tile adds them in order
-        const int64_t mine = ((int64_t)(u.part + u.split) * a.H + h) * BQ;
+        const int64_t mine = r.part_at(u.part + u.split, a.H, h, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * ty + i;
@@ -116,10 +116,10 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
             const int row = i / DV, c = i % DV;
             float M = -INFINITY, L = 0.f, O = 0.f;
             for (int s = 0; s < u.nsplit; ++s)
-                M = fmaxf(M, __ldcg(&r.part_ml[((int64_t)(u.part + s) * a.H + h) * BQ + row].x));
+                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part + s, a.H, h, row)].x));
             const float base = M == -INFINITY ? 0.f : M;
             for (int s = 0; s < u.nsplit; ++s) {
-                const int64_t at = ((int64_t)(u.part + s) * a.H + h) * BQ + row;
+                const int64_t at = r.part_at(u.part + s, a.H, h, row);
                 const float2 ml = __ldcg(&r.part_ml[at]);
                 const float w = exp2f(ml.x - base);
                 L = fmaf(ml.y, w, L);
