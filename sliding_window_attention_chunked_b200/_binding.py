@@ -7,6 +7,7 @@ the computation itself is entirely inside the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -497,71 +498,91 @@ def swska_cache_fill_fp8(k, v, k_cache, v_cache, window, k_scale=1.0, v_scale=1.
     return k_cache, v_cache
 
 
-def _same_device(ref, name, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{n} is on {t.device}, {name} on {ref.device}")
+def _expect(device, *items):
+    """Checks tensors given as (name, tensor, dtype, shape): contiguous, on CUDA device `device` (an
+    index), of that dtype and shape. One test per tensor; the reason is found only when it fails."""
+    for name, t, dtype, shape in items:
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                or t.get_device() != device):
+            _need(t, name, dtype, len(shape))
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+            raise ValueError(f"{name} is on {t.device}, the others on cuda:{device}")
 
 
-def _stream_on(stream, device):
-    """The stream to launch on: the caller's, else the current one of the tensors' device."""
-    return ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+def _index(t, name):
+    """The CUDA device index of the tensor that the others have to be with."""
+    _need(t, name)
+    return t.get_device()
+
+
+def _launch(device, stream, fn, *args):
+    """Calls a library function with the stream appended (the caller's, else the current one of the
+    tensors' device), with that device current."""
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        return fn(*args, raw)
+    with torch.cuda.device(device):
+        return fn(*args, raw)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(device, fn, *sizes):
+    """A workspace size (a fixed function of the sizes and the device), at least 16 bytes."""
+    with torch.cuda.device(device):
+        return max(int(getattr(load_library(), fn)(*sizes)), 16)
+
+
+def _workspace(given, device, fn, *sizes):
+    if given is None:
+        return torch.empty(_workspace_bytes(device, fn, *sizes), dtype=torch.uint8, device=device)
+    _need(given, "workspace")
+    if given.get_device() != device:
+        raise ValueError(f"workspace is on {given.device}, the others on cuda:{device}")
+    return given
 
 
 def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, stream=None):
     """swska_prefill_lse whose first ``sinks`` tokens (0 .. 128) stay visible to every later query:
     q [B,H,T,dk], k [B,T,dk] (shared by the heads), v [B,H,T,dv]. Returns (o [B,H,T,dv],
     lse [B,H,T] fp32), the pair swska_sink_backward takes."""
+    dev, dt = _index(q, "q"), q.dtype
     _need(q, "q", None, 4)
-    _need(k, "k", q.dtype, 3)
-    _need(v, "v", q.dtype, 4)
+    _need(v, "v", dt, 4)
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    if tuple(k.shape) != (B, T, dk) or tuple(v.shape[:3]) != (B, H, T):
-        raise ValueError("k must be [B,T,dk] and v [B,H,T,dv]")
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        o = torch.empty((B, H, T, dv), dtype=dt, device=q.device)
     if lse is None:
         lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    _need(o, "o", q.dtype, 4)
-    _need(lse, "lse", torch.float32, 3)
-    if tuple(o.shape) != (B, H, T, dv) or tuple(lse.shape) != (B, H, T):
-        raise ValueError("o must be [B,H,T,dv] and lse [B,H,T]")
-    _same_device(q, "q", k=k, v=v, o=o, lse=lse)
-    with torch.cuda.device(q.device):
-        st = load_library().rod_swska_sink_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, dk, dv,
-                                                   int(window), int(sinks), float(scale or 0.0), _dtype_code(q),
-                                                   _stream_on(stream, q.device))
-    _raise_on("rod_swska_sink_prefill", st)
+    _expect(dev, ("k", k, dt, (B, T, dk)), ("v", v, dt, (B, H, T, dv)), ("o", o, dt, (B, H, T, dv)),
+            ("lse", lse, torch.float32, (B, H, T)))
+    _raise_on("rod_swska_sink_prefill",
+              _launch(dev, stream, load_library().rod_swska_sink_prefill, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      o.data_ptr(), lse.data_ptr(), B, H, T, dk, dv, int(window), int(sinks), float(scale or 0.0),
+                      _dtype_code(q)))
     return o, lse
 
 
 def swska_sink_backward(q, k, v, o, lse, dO, window, sinks, scale=None, workspace=None, stream=None):
     """Gradients of swska_sink_prefill from its o and lse (same q, k, v, window, sinks and scale) and
     the loss gradient dO [B,H,T,dv]. Returns (dq, dk, dv) in the layouts and dtype of q, k, v."""
+    dev, dt = _index(q, "q"), q.dtype
     _need(q, "q", None, 4)
-    _need(k, "k", q.dtype, 3)
-    for n, t in (("v", v), ("o", o), ("dO", dO)):
-        _need(t, n, q.dtype, 4)
-    _need(lse, "lse", torch.float32, 3)
+    _need(v, "v", dt, 4)
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    if (tuple(k.shape) != (B, T, dk) or tuple(v.shape[:3]) != (B, H, T) or tuple(dO.shape) != tuple(v.shape)
-            or tuple(o.shape) != tuple(v.shape) or tuple(lse.shape) != (B, H, T)):
-        raise ValueError("shape mismatch")
-    _same_device(q, "q", k=k, v=v, o=o, lse=lse, dO=dO, workspace=workspace)
-    lib = load_library()
+    rows = (B, H, T, dv)
+    _expect(dev, ("k", k, dt, (B, T, dk)), ("v", v, dt, rows), ("o", o, dt, rows), ("dO", dO, dt, rows),
+            ("lse", lse, torch.float32, (B, H, T)))
+    code, window, sinks = _dtype_code(q), int(window), int(sinks)
+    ws = _workspace(workspace, dev, "rod_swska_sink_backward_workspace_size", B, H, T, dk, dv, window, sinks)
     dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            need = lib.rod_swska_sink_backward_workspace_size(B, H, T, dk, dv, int(window), int(sinks))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        st = lib.rod_swska_sink_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq),
-                                         _ptr(dk_), _ptr(dv_), B, H, T, dk, dv, int(window), int(sinks),
-                                         float(scale or 0.0), _dtype_code(q), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(),
-                                         _stream_on(stream, q.device))
-    _raise_on("rod_swska_sink_backward", st)
+    _raise_on("rod_swska_sink_backward",
+              _launch(dev, stream, load_library().rod_swska_sink_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      o.data_ptr(), lse.data_ptr(), dO.data_ptr(), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), B, H,
+                      T, dk, dv, window, sinks, float(scale or 0.0), code, ws.data_ptr(),
+                      ws.numel() * ws.element_size()))
     return dq, dk_, dv_
 
 
@@ -576,50 +597,38 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     j < sinks. max_len: a bound on the new tokens of one sequence (default M). k_new, v_new and
     slot_map may all be None: the cache has the tokens. Returns o [M,H,dv]; rows past
     cu_seqlens[N] are not written. The tables come from swska_page_tables."""
+    dev, dt = _index(q, "q"), q.dtype
     _need(q, "q", None, 3)
-    _need(k_pool, "k_pool", q.dtype, 3)
-    _need(v_pool, "v_pool", q.dtype, 4)
+    _need(v_pool, "v_pool", dt, 4)
     _need(block_table, "block_table", torch.int32, 2)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    _need(ctx, "ctx", torch.int64, 1)
     M, H, dk = q.shape
-    P, page, dv = k_pool.shape[0], k_pool.shape[1], v_pool.shape[-1]
+    P, _, page, dv = v_pool.shape
     N, max_pages = block_table.shape
-    if (k_new is None) != (v_new is None) or (k_new is None) != (slot_map is None):
-        raise ValueError("k_new, v_new and slot_map come together or not at all")
-    if k_new is not None:
-        _need(k_new, "k_new", q.dtype, 2)
-        _need(v_new, "v_new", q.dtype, 3)
-        _need(slot_map, "slot_map", torch.int32, 1)
-        if tuple(k_new.shape) != (M, dk) or tuple(v_new.shape) != (M, H, dv) or slot_map.shape[0] != M:
-            raise ValueError("k_new must be [M,dk], v_new [M,H,dv] and slot_map [M]")
-    if (k_pool.shape[2] != dk or tuple(v_pool.shape[:3]) != (P, H, page) or cu_seqlens.shape[0] != N + 1
-            or ctx.shape[0] != N):
-        raise ValueError("shape mismatch")
     if o is None:
-        o = torch.empty((M, H, dv), dtype=q.dtype, device=q.device)
-    _need(o, "o", q.dtype, 3)
-    if tuple(o.shape) != (M, H, dv):
-        raise ValueError("o must be [M,H,dv]")
-    if max_len is not None and max_len < 0:
-        raise ValueError("max_len must not be negative")
+        o = torch.empty((M, H, dv), dtype=dt, device=q.device)
+    _expect(dev, ("k_pool", k_pool, dt, (P, page, dk)), ("v_pool", v_pool, dt, (P, H, page, dv)),
+            ("block_table", block_table, torch.int32, (N, max_pages)), ("ctx", ctx, torch.int64, (N,)),
+            ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,)), ("o", o, dt, (M, H, dv)))
+    if k_new is not None and v_new is not None and slot_map is not None:
+        _expect(dev, ("k_new", k_new, dt, (M, dk)), ("v_new", v_new, dt, (M, H, dv)),
+                ("slot_map", slot_map, torch.int32, (M,)))
+        new = k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr()
+    elif k_new is None and v_new is None and slot_map is None:
+        new = None, None, None
+    else:
+        raise ValueError("k_new, v_new and slot_map come together or not at all")
     most = M if max_len is None else int(max_len)
+    if most < 0:
+        raise ValueError("max_len must not be negative")
     if most == 0:
         return o  # no sequence has a new token
-    _same_device(q, "q", k_new=k_new, v_new=v_new, k_pool=k_pool, v_pool=v_pool, block_table=block_table,
-                 slot_map=slot_map, cu_seqlens=cu_seqlens, ctx=ctx, o=o, workspace=workspace)
-    lib = load_library()
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            need = lib.rod_swska_extend_paged_workspace_size(M, N, H, dk, dv, most, _dtype_code(q))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        st = lib.rod_swska_extend_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
-                                        _ptr(block_table), _ptr(slot_map), _ptr(cu_seqlens), _ptr(ctx), _ptr(o),
-                                        M, N, H, dk, dv, P, page, max_pages, int(window), int(sinks), most,
-                                        float(scale or 0.0), _dtype_code(q), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(),
-                                        _stream_on(stream, q.device))
-    _raise_on("rod_swska_extend_paged", st)
+    code = _dtype_code(q)
+    ws = _workspace(workspace, dev, "rod_swska_extend_paged_workspace_size", M, N, H, dk, dv, most, code)
+    _raise_on("rod_swska_extend_paged",
+              _launch(dev, stream, load_library().rod_swska_extend_paged, q.data_ptr(), new[0], new[1],
+                      k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), new[2], cu_seqlens.data_ptr(),
+                      ctx.data_ptr(), o.data_ptr(), M, N, H, dk, dv, P, page, max_pages, int(window), int(sinks), most,
+                      float(scale or 0.0), code, ws.data_ptr(), ws.numel() * ws.element_size()))
     return o
 
 
@@ -631,30 +640,24 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     (past the first ``sinks`` tokens) go back to the free list, pages for the new tokens are taken
     from it. Returns (cu_seqlens [N+1], slot_map [max_tokens]) int32 for swska_extend_paged; a
     sequence for which pages or tokens run out is served none this step."""
-    _need(ctx, "ctx", torch.int64, 1)
-    for n, t, nd in (("n_new", n_new, 1), ("block_table", block_table, 2), ("first", first, 1),
-                     ("free_list", free_list, 1), ("free_count", free_count, 1)):
-        _need(t, n, torch.int32, nd)
+    dev, i32 = _index(ctx, "ctx"), torch.int32
+    _need(block_table, "block_table", i32, 2)
+    _need(free_list, "free_list", i32, 1)
     N, max_pages = block_table.shape
-    if ctx.shape[0] != N or n_new.shape[0] != N or first.shape[0] != N or free_count.shape[0] != 1:
-        raise ValueError("shape mismatch")
-    M = int(max_tokens)
+    P, M = free_list.shape[0], int(max_tokens)
     if M < 0:
         raise ValueError("max_tokens must not be negative")
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(N + 1, dtype=torch.int32, device=ctx.device)
+        cu_seqlens = torch.empty(N + 1, dtype=i32, device=ctx.device)
     if slot_map is None:
-        slot_map = torch.empty(M, dtype=torch.int32, device=ctx.device)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    _need(slot_map, "slot_map", torch.int32, 1)
-    if cu_seqlens.shape[0] != N + 1 or slot_map.shape[0] != M:
-        raise ValueError("cu_seqlens must be [N+1] and slot_map [max_tokens]")
-    _same_device(ctx, "ctx", n_new=n_new, block_table=block_table, first=first, free_list=free_list,
-                 free_count=free_count, cu_seqlens=cu_seqlens, slot_map=slot_map)
-    with torch.cuda.device(ctx.device):
-        st = load_library().rod_swska_page_tables(_ptr(ctx), _ptr(n_new), _ptr(block_table), _ptr(first),
-                                                  _ptr(free_list), _ptr(free_count), _ptr(cu_seqlens),
-                                                  _ptr(slot_map), N, max_pages, free_list.shape[0], int(page_size),
-                                                  int(window), int(sinks), M, _stream_on(stream, ctx.device))
-    _raise_on("rod_swska_page_tables", st)
+        slot_map = torch.empty(M, dtype=i32, device=ctx.device)
+    _expect(dev, ("ctx", ctx, torch.int64, (N,)), ("n_new", n_new, i32, (N,)),
+            ("block_table", block_table, i32, (N, max_pages)), ("first", first, i32, (N,)),
+            ("free_list", free_list, i32, (P,)), ("free_count", free_count, i32, (1,)),
+            ("cu_seqlens", cu_seqlens, i32, (N + 1,)), ("slot_map", slot_map, i32, (M,)))
+    _raise_on("rod_swska_page_tables",
+              _launch(dev, stream, load_library().rod_swska_page_tables, ctx.data_ptr(), n_new.data_ptr(),
+                      block_table.data_ptr(), first.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
+                      cu_seqlens.data_ptr(), slot_map.data_ptr(), N, max_pages, P, int(page_size), int(window),
+                      int(sinks), M))
     return cu_seqlens, slot_map

@@ -2,12 +2,14 @@
 //
 // A query tile is up to `rows` new tokens of one sequence; it visits the key tiles (tile keys at
 // positions that are multiples of `tile`) of the first S tokens that lie before its window, then
-// those of the window. Where the batch has fewer query tiles x head groups than the GPU has room
-// for, a tile's keys are split into units of neighbouring key tiles; each unit leaves its rows'
-// maxima, sums and unnormalised outputs in fp32, and the unit that finishes last (a counter per
-// tile and head) adds them in the order of the keys, so the result does not depend on timing.
-// The division depends on the lengths, which live on the device, so the launch that writes the new
-// tokens to the cache also makes the list of units.
+// those of the window. The CTAs of a head group share this work evenly whatever the lengths are: all
+// key tiles of all query tiles stand in one line, which is cut into `cols` chunks of equal length, one
+// per CTA. A query tile that a cut goes through is split: each CTA leaves its rows' maxima, sums
+// and unnormalised outputs in fp32, and the one that finishes last (a counter per tile and head)
+// adds them in the order of the keys, so the result does not depend on timing. A CTA has at most two
+// such parts (of its first and its last query tile), which bounds the workspace by the GPU, not
+// by the batch. The division depends on the lengths, which live on the device, so the launch that
+// writes the new tokens to the cache also makes the list of units (query tile x chunk).
 #pragma once
 
 #include "common.cuh"
@@ -16,36 +18,43 @@
 namespace rod {
 
 struct ExtendUnit {  // 48 bytes: all that a CTA needs besides the table, so that it waits for one load
-    int n, q0;       // sequence, its first query of the tile
-    int kt0, kt1;    // this unit's range in the tile's list of key tiles
-    int part;        // first part of the tile (parts are numbered like units), -1: not split
-    int nsplit;
-    int split;
-    int item;        // the tile's counter row
-    int row0, len, ctx, pad;  // of the sequence (ExtendSeq)
+    int n, q0;          // sequence, its first query of the tile
+    int kt0, kt1;       // this unit's range in the tile's list of key tiles (may be empty)
+    int part, first;    // this unit's part and the tile's first, -1: the tile is not split
+    int c0, nsplit;     // chunk of the first part, parts: the others have numbers 2 (c0 + 1), 2 (c0 + 2), ...
+    int row0, len, ctx; // of the sequence (ExtendSeq)
+    int counter;
+    __device__ __forceinline__ int part_of(int s) const { return s == 0 ? first : 2 * (c0 + s); }
 };
 
 struct ExtendRoute {
     int rows = 0, tile = 0;  // queries per tile (0: route not used), keys per key tile
-    int groups = 1;          // head groups: CTAs per unit
-    int target = 1;          // units x groups to reach by splitting, in units of at least
-    int share = 1;           // min(min_tiles, all tiles / share) key tiles
-    int min_tiles = 1;
+    int groups = 1;          // head groups
+    int cols = 1;            // CTAs per head group
+    int min_chunk = 1;       // key tiles that a CTA takes at least
     int part_rows = 0;       // rows kept of a part
-    int cap_units = 0, cap_items = 0, cap_parts = 0;
-    ExtendUnit* units = nullptr;
-    int* n_units = nullptr;
-    int* count = nullptr;    // [cap_items_split][H]
-    float* part_o = nullptr; // [cap_parts][H][part_rows][dv]
-    float2* part_ml = nullptr;  // [cap_parts][H][part_rows]: maximum (base 2) and sum
-    __device__ __forceinline__ int64_t part_at(int unit, int H, int h, int row) const {
-        return ((int64_t)unit * H + h) * part_rows + row;
+    int cap_items = 0;
+    ExtendUnit* units = nullptr;  // [cap_items + cols]: unit of query tile i in chunk c at i + c
+    int* range = nullptr;         // [cols][2]: first and last query tile of each chunk (first > last: none)
+    int* count = nullptr;         // [cols][H]
+    float* part_o = nullptr;      // [2 cols][H][part_rows][dv]
+    float2* part_ml = nullptr;    // [2 cols][H][part_rows]: maximum (base 2) and sum
+    __device__ __forceinline__ int64_t part_at(int part, int H, int h, int row) const {
+        return ((int64_t)part * H + h) * part_rows + row;
     }
 };
 __device__ __forceinline__ ExtendUnit load_unit(const ExtendUnit* p) {
     const int4* x = reinterpret_cast<const int4*>(p);
     const int4 a = __ldcg(x), b = __ldcg(x + 1), c = __ldcg(x + 2);
     return ExtendUnit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+}
+// the units of a CTA: x in [lo, hi]
+struct ExtendRange {
+    int lo, hi;
+};
+__device__ __forceinline__ ExtendRange load_range(const ExtendRoute& r, int col) {
+    const int2 t = __ldcg(reinterpret_cast<const int2*>(r.range) + col);
+    return ExtendRange{t.x + col, t.y + col};
 }
 
 struct ExtendPlan {

@@ -96,84 +96,112 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
     }
     // ---- the units of each route
     __shared__ int s_sums[NW];
-    __shared__ int s_at[NT + 1];     // first unit of each sequence of the chunk
-    __shared__ int s_items[NT + 1];  // first query tile
-    __shared__ int s_ns[NT];
+    __shared__ int s_at[NT];     // first unit of each sequence of the block of sequences
+    __shared__ int s_item[NT];   // first query tile
+    __shared__ unsigned s_v[NT]; // first key tile in the line
     for (int i = 0; i < 2; ++i) {
         const ExtendRoute& r = p.r[i];
         if (r.rows == 0) continue;
-        long long tiles = 0;
-        int items = 0;
-        for (int n = threadIdx.x; n < a.N; n += NT) {
-            const SeqWork w = seq_work(a, p, i, extend_seq(a, n));
-            items += w.items;
-            tiles += (long long)w.items * w.tiles;
+        // the line of all key tiles; a length is halved until it fits 31 bits (a split is proportional)
+        int shift = 0, items = 0;
+        unsigned V = 0;
+        for (;;) {
+            long long v = 0;
+            int it = 0;
+            for (int n = threadIdx.x; n < a.N; n += NT) {
+                const SeqWork w = seq_work(a, p, i, extend_seq(a, n));
+                it += w.items;
+                v += (long long)w.items * ((w.tiles >> shift) + (shift > 0));
+            }
+            int lo, hi;
+            block_incl(it, s_sums, &items);
+            block_incl((int)(v & 0xffff), s_sums, &lo);
+            block_incl((int)(v >> 16 < 0x3fffff ? v >> 16 : 0x3fffff), s_sums, &hi);
+            const long long all = ((long long)hi << 16) + lo;
+            V = (unsigned)all;
+            if (all < 0x7fffffff) break;
+            ++shift;
         }
-        int n_items, lo, hi;
-        block_incl(items, s_sums, &n_items);
-        // the sum of up to 2^47 in two halves
-        block_incl((int)(tiles & 0xffff), s_sums, &lo);
-        block_incl((int)(tiles >> 16), s_sums, &hi);
-        const long long n_tiles = ((long long)hi << 16) + lo;
-        // key tiles per unit: enough units for the GPU, and no split when the query tiles do
-        long long C = 1ll << 40;
-        if ((long long)n_items * r.groups < r.target) {
-            C = (n_tiles * r.groups + r.target - 1) / r.target;
-            const long long even = (n_tiles * r.groups + r.share - 1) / r.share;
-            const long long least = even < r.min_tiles ? even : r.min_tiles;
-            if (C < least) C = least;
-            if (C < 1) C = 1;
-            for (int x = threadIdx.x; x < n_items * a.H; x += NT) r.count[x] = 0;
-        }
-        int units = 0, item0 = 0;
+        const unsigned even = (V + r.cols - 1) / r.cols;
+        const unsigned Q = even > (unsigned)r.min_chunk ? even : r.min_chunk;
+        for (int x = threadIdx.x; x < r.cols * a.H; x += NT) r.count[x] = 0;
+        for (int c = threadIdx.x; c < r.cols; c += NT)
+            if (c * (unsigned long long)Q >= V) reinterpret_cast<int2*>(r.range)[c] = make_int2(1, 0);
+        unsigned v_done = 0;
+        int i_done = 0;
         for (int base = 0; base < a.N; base += NT) {
             const int n = base + (int)threadIdx.x;
             SeqWork w{0, 0};
             if (n < a.N) w = seq_work(a, p, i, extend_seq(a, n));
-            const int ns = w.items > 0 ? (int)((w.tiles + C - 1) / C) : 1;
-            int tot_u, tot_i;
-            const int at = block_incl(w.items * ns, s_sums, &tot_u);
-            const int it = block_incl(w.items, s_sums, &tot_i);
-            s_at[threadIdx.x] = at - w.items * ns;
-            s_items[threadIdx.x] = item0 + it - w.items;
-            s_ns[threadIdx.x] = ns;
-            if (threadIdx.x == NT - 1) s_at[NT] = at;
+            const int t = w.items ? (w.tiles >> shift) + (shift > 0) : 0;
+            int tot_i, tot_v;
+            const int it = i_done + block_incl(w.items, s_sums, &tot_i) - w.items;
+            const unsigned v0 = v_done + (unsigned)(block_incl(w.items * t, s_sums, &tot_v) - w.items * t);
+            s_item[threadIdx.x] = it;
+            s_v[threadIdx.x] = v0;
+            s_at[threadIdx.x] = it + (int)(v0 / Q);
             __syncthreads();
-            for (int u = threadIdx.x; u < tot_u; u += NT) {
-                int l = 0, h = NT - 1;  // the last sequence that starts at or before u
+            // the sequence of the block at a place of an array of firsts (ties: the last, which has items)
+            auto find = [&](auto* first, auto x) {
+                int l = 0, h = NT - 1;
                 while (l < h) {
                     const int m = (l + h + 1) >> 1;
-                    if (s_at[m] <= u) l = m;
+                    if (first[m] <= x) l = m;
                     else h = m - 1;
                 }
-                const int nsp = s_ns[l], local = u - s_at[l];
-                ExtendUnit e;
-                e.n = base + l;
-                e.q0 = local / nsp * r.rows;
-                e.split = local % nsp;
-                e.nsplit = nsp;
-                e.item = s_items[l] + local / nsp;
-                const int at_u = units + u;
-                e.part = nsp > 1 ? at_u - e.split : -1;
-                const ExtendSeq sq = extend_seq(a, e.n);
-                e.row0 = sq.row0;
-                e.len = sq.len;
-                e.ctx = sq.ctx;
-                const ExtendKeys k = extend_keys(sq, e.q0, r.rows, r.tile, a.W, a.S);
-                e.kt0 = (int)((long long)e.split * k.n / nsp);
-                e.kt1 = (int)((long long)(e.split + 1) * k.n / nsp);
-                if (at_u < r.cap_units) {
-                    int4* to = reinterpret_cast<int4*>(r.units + at_u);
-                    to[0] = make_int4(e.n, e.q0, e.kt0, e.kt1);
-                    to[1] = make_int4(e.part, e.nsplit, e.split, e.item);
-                    to[2] = make_int4(e.row0, e.len, e.ctx, 0);
+                return l;
+            };
+            auto tiles_of = [&](int l) {
+                const SeqWork x = seq_work(a, p, i, extend_seq(a, base + l));
+                return (unsigned)((x.tiles >> shift) + (shift > 0));
+            };
+            if (tot_i > 0) {
+                const unsigned vb = v_done, ve = v_done + (unsigned)tot_v;
+                for (int c = threadIdx.x; c < r.cols; c += NT) {
+                    const unsigned long long b64 = (unsigned long long)c * Q;
+                    if (b64 >= V) break;
+                    const unsigned b = (unsigned)b64, e = (V - b > Q ? b + Q : V) - 1;
+                    if (b >= vb && b < ve) {
+                        const int l = find(s_v, b);
+                        r.range[2 * c] = s_item[l] + (int)((b - s_v[l]) / tiles_of(l));
+                    }
+                    if (e >= vb && e < ve) {
+                        const int l = find(s_v, e);
+                        r.range[2 * c + 1] = s_item[l] + (int)((e - s_v[l]) / tiles_of(l));
+                    }
+                }
+                const int id_end = i_done + tot_i - 1 + (int)((ve - 1) / Q);
+                for (int id = s_at[0] + (int)threadIdx.x; id <= id_end; id += NT) {
+                    const int l = find(s_at, id);
+                    const ExtendSeq sq = extend_seq(a, base + l);
+                    const SeqWork w2 = seq_work(a, p, i, sq);
+                    const unsigned t2 = (unsigned)((w2.tiles >> shift) + (shift > 0)), vs = s_v[l];
+                    if (w2.items == 0) continue;
+                    int lo = 0, hi = w2.items - 1;  // the query tile: the last whose first unit is at or before id
+                    while (lo < hi) {
+                        const int m = (lo + hi + 1) >> 1;
+                        if (s_item[l] + m + (int)((vs + m * t2) / Q) <= id) lo = m;
+                        else hi = m - 1;
+                    }
+                    const unsigned b = vs + lo * t2, e = b + t2 - 1, c = (unsigned)(id - s_item[l] - lo);
+                    const unsigned c0 = b / Q, c1 = e / Q;
+                    if (c < c0 || c > c1) continue;  // a cut between two tiles: no unit there
+                    const ExtendKeys k = extend_keys(sq, lo * r.rows, r.rows, r.tile, a.W, a.S);
+                    const unsigned x0 = c * Q > b ? c * Q - b : 0, x1 = e - b + 1 < (c + 1) * Q - b ? t2 : (c + 1) * Q - b;
+                    const int kt0 = (int)((unsigned long long)x0 * k.n / t2), kt1 = (int)((unsigned long long)x1 * k.n / t2);
+                    // parts of chunk x: 2 x for its first query tile, 2 x + 1 for a later one (its last)
+                    const int first = 2 * (int)c0 + (c0 * Q == b || c0 * Q > b ? 0 : 1);
+                    const bool split = c0 != c1;
+                    int4* to = reinterpret_cast<int4*>(r.units + id);
+                    to[0] = make_int4(base + l, lo * r.rows, kt0, kt1);
+                    to[1] = make_int4(split ? (c == c0 ? first : 2 * (int)c) : -1, split ? first : -1, (int)c0, (int)(c1 - c0 + 1));
+                    to[2] = make_int4(sq.row0, sq.len, sq.ctx, (int)c1);
                 }
             }
-            units += tot_u;
-            item0 += tot_i;
+            v_done += (unsigned)tot_v;
+            i_done += tot_i;
             __syncthreads();
         }
-        if (threadIdx.x == 0) *r.n_units = units < r.cap_units ? units : r.cap_units;
     }
 }
 
@@ -184,55 +212,45 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf16) {
     ExtendPlan p;
     if (max_len > M) max_len = M;
-    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int target, int share, int min_tiles,
-                     int64_t items) {
+    // ctas: what the GPU holds at once
+    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int64_t items) {
         ExtendRoute& r = p.r[i];
         r.rows = rows;
+        r.part_rows = part_rows;
         r.tile = tile;
         r.groups = groups;
-        r.part_rows = part_rows;
-        r.target = target;
-        r.share = share;
-        r.min_tiles = min_tiles;
-        r.cap_items = (int)items;
-        // split units: at most one per query tile and target / groups more (sum of ceil(t / C))
-        const int split = 2 * (target / groups + 1);
-        r.cap_units = items > split ? (int)items : split;
-        r.cap_parts = split;
+        r.cols = ctas / groups > 1 ? ctas / groups : 1;
+        r.min_chunk = min_chunk;
+        r.cap_items = (int)(items < M ? items : M);
     };
     const int sms = device_sm_count();
     if (bf16 && dk == 128 && dv == 128 && max_len <= kFewRows) {
-        // One CTA per SM. Units of equal length come in whole rounds, so a few rounds waste part of the
-        // last one; more, shorter units waste less and add parts of at most max_len rows per head.
-        const int few = max_len < kFewRows ? max_len : kFewRows;
-        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, few <= 4 ? 8 * sms : 2 * sms, sms, 8, N);
+        route(0, kFewRows, max_len, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 2, N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
     const int rows = max_len <= 16 ? 16 : 64;
-    int64_t items = (int64_t)M / rows + N;
-    if (items > M) items = M;
-    route(0, rows, rows, 64, H, 4 * sms, sms, 1, items);
+    route(0, rows, rows, 64, H, (rows == 16 ? 4 : 2) * sms, 1, (int64_t)M / rows + N);
     return p;
 }
 
 size_t extend_bind(ExtendPlan& p, int H, int dv, void* workspace) {
     char* w = static_cast<char*>(workspace);
-    size_t at = 256;
+    size_t at = 0;
     for (int i = 0; i < 2; ++i) {
         ExtendRoute& r = p.r[i];
         if (r.rows == 0) continue;
-        r.n_units = reinterpret_cast<int*>(w) + i;
         auto take = [&](size_t bytes) {
             char* q = w + at;
             at += up(bytes);
             return q;
         };
-        r.units = reinterpret_cast<ExtendUnit*>(take((size_t)r.cap_units * sizeof(ExtendUnit)));
-        // counters exist for split tiles only, and those are fewer than target / groups
-        r.count = reinterpret_cast<int*>(take((size_t)r.cap_parts * H * sizeof(int)));
-        r.part_ml = reinterpret_cast<float2*>(take((size_t)r.cap_parts * H * r.part_rows * sizeof(float2)));
-        r.part_o = reinterpret_cast<float*>(take((size_t)r.cap_parts * H * r.part_rows * dv * sizeof(float)));
+        const size_t parts = (size_t)2 * r.cols * H * r.part_rows;
+        r.units = reinterpret_cast<ExtendUnit*>(take((size_t)(r.cap_items + r.cols) * sizeof(ExtendUnit)));
+        r.range = reinterpret_cast<int*>(take((size_t)r.cols * 2 * sizeof(int)));
+        r.count = reinterpret_cast<int*>(take((size_t)r.cols * H * sizeof(int)));
+        r.part_ml = reinterpret_cast<float2*>(take(parts * sizeof(float2)));
+        r.part_o = reinterpret_cast<float*>(take(parts * dv * sizeof(float)));
     }
     return at;
 }

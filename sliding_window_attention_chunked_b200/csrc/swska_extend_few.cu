@@ -3,7 +3,7 @@
 //
 //   o[i,h] = sum_j softmax_j(scale q[i,h] . k[j]) v[h,j],  j <= p, j > p - W or j < S,  p = ctx + i
 // Few queries against a window of keys: every value row is used for at most 16 dot products, so the
-// kernel is bound by reading the cache (values: H times the keys) from HBM. A CTA takes a unit (one
+// kernel is bound by reading the cache (values: H times the keys) from HBM. A CTA takes units (one
 // sequence, some key tiles of 32) of up to eight heads, so that the shared key tile is fetched once
 // for them: one warp per head, which multiplies with m16n8k16 instructions (16 query rows; a
 // tcgen05 tile of 128 rows would be seven eighths padding), and one warp that feeds a ring of
@@ -83,7 +83,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int stage_bytes = TILE * (1 + hpg);
 
     // a CTA keeps to one head group: blockIdx.x = group + groups * column
-    const int grp = blockIdx.x % r.groups, cols = gridDim.x / r.groups;
+    const int grp = blockIdx.x % r.groups;
     const int h0 = grp * hpg, nh = min(hpg, a.H - h0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < n_stages; ++s) {
@@ -95,7 +95,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
     __syncthreads();
     wait_for_launch_before();
-    const int n_units = __ldcg(r.n_units);
+    const ExtendRange range = load_range(r, blockIdx.x / r.groups);
 
     if (warp == kFewHeads) {
         // ------------------------------- producer -------------------------------
@@ -106,7 +106,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int nbox = KT / box, ops = 2 * nbox * (1 + nh);
         int t = 0;  // tiles fed so far
         bool ok = true;
-        for (int x = blockIdx.x / r.groups; x < n_units && ok; x += cols) {
+        for (int x = range.lo; x <= range.hi && ok; ++x) {
             const ExtendUnit u = load_unit(r.units + x);
             const ExtendSeq sq{u.row0, u.len, u.ctx, false};
             const ExtendKeys kt = extend_keys(sq, u.q0, kFewRows, KT, a.W, a.S);
@@ -153,7 +153,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int g = lane / 4, c2 = 2 * (lane % 4);  // this thread's rows g, g + 8 and its column pair
     const int mat = lane / 8, mr = lane % 8;      // this lane's row address in a 4-matrix load
     int t = 0;
-    for (int x = blockIdx.x / r.groups; x < n_units; x += cols) {
+    for (int x = range.lo; x <= range.hi; ++x) {
         const ExtendUnit u = load_unit(r.units + x);
         const ExtendSeq sq{u.row0, u.len, u.ctx, false};
         const ExtendKeys kt = extend_keys(sq, u.q0, kFewRows, KT, a.W, a.S);
@@ -304,7 +304,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int e = 0; e < 2; ++e) {
             const int row = g + 8 * e;
             if (row >= rows) continue;
-            const int64_t at = r.part_at(u.part + u.split, a.H, h, row);
+            const int64_t at = r.part_at(u.part, a.H, h, row);
             if (lane % 4 == 0) r.part_ml[at] = make_float2(m[e], l[e]);
 #pragma unroll
             for (int c = 0; c < 16; ++c)
@@ -313,13 +313,13 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __threadfence();
         __syncwarp();
         int last = 0;
-        if (lane == 0) last = atomicAdd(r.count + (int64_t)u.item * a.H + h, 1) == u.nsplit - 1;
+        if (lane == 0) last = atomicAdd(r.count + (int64_t)u.counter * a.H + h, 1) == u.nsplit - 1;
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
         __threadfence();
         for (int row = 0; row < rows; ++row) {
             float M = -INFINITY;
             for (int s = lane; s < u.nsplit; s += 32)
-                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part + s, a.H, h, row)].x));
+                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, h, row)].x));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
             const float base = M == -INFINITY ? 0.f : M;
@@ -327,7 +327,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int s = 0; s < u.nsplit; ++s) {
-                const int64_t at = r.part_at(u.part + s, a.H, h, row);
+                const int64_t at = r.part_at(u.part_of(s), a.H, h, row);
                 const float2 ml = __ldcg(&r.part_ml[at]);
                 const float4 x4 = __ldcg(reinterpret_cast<const float4*>(r.part_o + at * HD) + lane);
                 const float w = tc::ex2(ml.x - base);
@@ -356,13 +356,8 @@ cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, c
     int stages = RING / (TILE * (1 + hpg));
     if (stages > MAXST) stages = MAXST;
     if ((e = cudaFuncSetAttribute(extend_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
-    // every column of CTAs covers all head groups; one CTA per SM
-    const int64_t want = r.cap_units;
-    int64_t cols = device_sm_count() / r.groups;
-    if (cols < 1) cols = 1;
-    if (cols > want) cols = want;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(cols * r.groups));
+    cfg.gridDim = dim3((unsigned)(r.cols * r.groups));  // one CTA per SM
     cfg.blockDim = dim3(NTH);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = s;

@@ -34,10 +34,10 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
     int* sAt = reinterpret_cast<int*>(sP + BQ * LDP);  // slot of each key of the tile, -1: none
     int* sLast = sAt + BK;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const int n_work = *r.n_units * a.H;
-    for (int x = blockIdx.x; x < n_work; x += gridDim.x) {
-        const ExtendUnit u = load_unit(r.units + x / a.H);
-        const int h = x % a.H;
+    const int h = blockIdx.x % a.H;
+    const ExtendRange range = load_range(r, blockIdx.x / a.H);
+    for (int x = range.lo; x <= range.hi; ++x) {
+        const ExtendUnit u = load_unit(r.units + x);
         const ExtendSeq sq{u.row0, u.len, u.ctx, false};
         const int rows = sq.len - u.q0 < BQ ? sq.len - u.q0 : BQ;
         const int p0 = sq.ctx + u.q0, p1 = p0 + rows - 1;
@@ -97,7 +97,7 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
             continue;
         }
         // this unit's part, then the last unit of the tile adds them in order
-        const int64_t mine = r.part_at(u.part + u.split, a.H, h, 0);
+        const int64_t mine = r.part_at(u.part, a.H, h, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * ty + i;
@@ -108,7 +108,7 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
         }
         __threadfence();
         __syncthreads();
-        if (threadIdx.x == 0) *sLast = atomicAdd(r.count + (int64_t)u.item * a.H + h, 1) == u.nsplit - 1;
+        if (threadIdx.x == 0) *sLast = atomicAdd(r.count + (int64_t)u.counter * a.H + h, 1) == u.nsplit - 1;
         __syncthreads();
         if (!*sLast) continue;
         __threadfence();
@@ -116,10 +116,10 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
             const int row = i / DV, c = i % DV;
             float M = -INFINITY, L = 0.f, O = 0.f;
             for (int s = 0; s < u.nsplit; ++s)
-                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part + s, a.H, h, row)].x));
+                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, h, row)].x));
             const float base = M == -INFINITY ? 0.f : M;
             for (int s = 0; s < u.nsplit; ++s) {
-                const int64_t at = r.part_at(u.part + s, a.H, h, row);
+                const int64_t at = r.part_at(u.part_of(s), a.H, h, row);
                 const float2 ml = __ldcg(&r.part_ml[at]);
                 const float w = exp2f(ml.x - base);
                 L = fmaf(ml.y, w, L);
@@ -135,9 +135,7 @@ cudaError_t launch_t(const ExtendArgs& a, const ExtendRoute& r, bool bf16, cudaS
     constexpr int smem = smem_bytes<DK, DV, BQ>();
     cudaError_t e = cudaFuncSetAttribute(extend_simt_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t want = (int64_t)r.cap_units * a.H;
-    const int64_t cap = (int64_t)device_sm_count() * (BQ == 64 ? 2 : 4);
-    extend_simt_kernel<DK, DV, BQ><<<(unsigned)(want < cap ? want : cap), 4 * BQ, smem, s>>>(
+    extend_simt_kernel<DK, DV, BQ><<<(unsigned)(r.cols * r.groups), 4 * BQ, smem, s>>>(
         a, r, bf16, a.scale * 1.4426950408889634f);
     note_launches(1);
     return cudaGetLastError();
