@@ -116,6 +116,10 @@ __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddep
 cudaError_t swska_extend_simt_launch(const ExtendArgs& a, const ExtendRoute& r, bool bf16, cudaStream_t s);
 cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, cudaStream_t s);
 unsigned swska_extend_few_take_timeout_flag();
+cudaError_t swska_extend_tc_launch(const ExtendArgs& a, const ExtendRoute& r, cudaStream_t s);
+unsigned swska_extend_tc_take_timeout_flag();
+constexpr int kChunkRows = 128;  // bf16, 128-wide heads: longer sequences, in tiles of so many queries
+constexpr int kChunkTile = 128;  // and keys
 constexpr int kFewRows = 16;   // bf16, 128-wide heads: sequences of at most this many new tokens
 constexpr int kFewTile = 32;   // keys per tile there
 constexpr int kFewHeads = 8;   // heads per CTA there

@@ -224,8 +224,12 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         r.cap_items = (int)(items < M ? items : M);
     };
     const int sms = device_sm_count();
-    if (bf16 && dk == 128 && dv == 128 && max_len <= kFewRows) {
-        route(0, kFewRows, max_len, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 2, N);
+    if (bf16 && dk == 128 && dv == 128) {
+        const int few = max_len < kFewRows ? max_len : kFewRows;
+        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 2, N);
+        p.short_len = kFewRows;
+        if (max_len > kFewRows)
+            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, (int64_t)M / kChunkRows + N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
@@ -269,10 +273,15 @@ cudaError_t swska_extend_launch(const ExtendArgs& a, bool bf16, cudaStream_t s) 
     note_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (p.r[0].tile == kFewTile) return swska_extend_few_launch(a, p.r[0], s);
+    if (p.r[0].tile == kFewTile) {
+        e = swska_extend_few_launch(a, p.r[0], s);
+        return e == cudaSuccess && p.r[1].rows ? swska_extend_tc_launch(a, p.r[1], s) : e;
+    }
     return swska_extend_simt_launch(a, p.r[0], bf16, s);
 }
 
-unsigned swska_extend_take_timeout_flag() { return swska_extend_few_take_timeout_flag(); }
+unsigned swska_extend_take_timeout_flag() {
+    return swska_extend_few_take_timeout_flag() | swska_extend_tc_take_timeout_flag();
+}
 
 }  // namespace rod
