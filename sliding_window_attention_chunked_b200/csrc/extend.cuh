@@ -91,10 +91,11 @@ __device__ __forceinline__ ExtendKeys extend_keys(const ExtendSeq& s, int q0, in
     const int p0 = s.ctx + q0, last = q0 + rows < s.len ? q0 + rows : s.len;
     const int p1 = s.ctx + last - 1;
     const int64_t lo = (int64_t)p0 - W + 1;
-    k.lo = (int)(lo > 0 ? lo : 0) / tile;
-    const int ns = (S + tile - 1) / tile;
+    const int tl = __ffs(tile) - 1;  // a power of two
+    k.lo = (int)(lo > 0 ? lo : 0) >> tl;
+    const int ns = (S + tile - 1) >> tl;
     k.n_sink = ns < k.lo ? ns : k.lo;
-    k.n = k.n_sink + p1 / tile - k.lo + 1;
+    k.n = k.n_sink + (p1 >> tl) - k.lo + 1;
     return k;
 }
 

@@ -14,43 +14,58 @@ namespace {
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
 
-__device__ __forceinline__ int block_incl(int x, int* sums, int* total) {
+// inclusive scan of a pair over the block, with the block's sums
+struct Pair {
+    int items;
+    long long v;
+};
+__device__ __forceinline__ Pair block_incl(Pair x, Pair* sums, Pair* total) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, x.items, d);
+        const long long z = __shfl_up_sync(0xffffffffu, x.v, d);
+        if (lane >= d) {
+            x.items += y;
+            x.v += z;
+        }
     }
     __syncthreads();
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
+    Pair all{0, 0};
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const int t = sums[w];
-        if (w < warp) before += t;
-        all += t;
+        const Pair t = sums[w];
+        if (w < warp) {
+            x.items += t.items;
+            x.v += t.v;
+        }
+        all.items += t.items;
+        all.v += t.v;
     }
     *total = all;
-    return x + before;
+    return x;
 }
 
-// query tiles and, at most, key tiles per query tile of a sequence on route i (0 tiles: not on it)
+// query tiles and, at most, key tiles per query tile of a sequence on route i (0 tiles: not on it);
+// rows and tile are powers of two
 struct SeqWork {
     int items, tiles;
 };
 __device__ __forceinline__ SeqWork seq_work(const ExtendArgs& a, const ExtendPlan& p, int i, const ExtendSeq& s) {
     const ExtendRoute& r = p.r[i];
     SeqWork w{0, 0};
-    if (s.len == 0 || s.bad || r.rows == 0) return w;
+    if (s.len == 0 || s.bad) return w;
     const bool is_short = p.r[0].rows != 0 && (s.len <= p.short_len || p.r[1].rows == 0);
     if (is_short != (i == 0)) return w;
-    w.items = (s.len + r.rows - 1) / r.rows;
+    const int rl = __ffs(r.rows) - 1, tl = __ffs(r.tile) - 1;
+    w.items = (s.len + r.rows - 1) >> rl;
     // the widest query tile: a window and the tile's rows, at any alignment, and the first tokens
     const int rows = s.len < r.rows ? s.len : r.rows;
     const int64_t span = (int64_t)(a.W < s.ctx + s.len ? a.W : s.ctx + s.len) + rows;
-    const int most = (int)((span + r.tile - 1) / r.tile) + 1 + (a.S + r.tile - 1) / r.tile;
-    const int all = (s.ctx + s.len - 1) / r.tile + 1;
+    const int most = (int)((span + r.tile - 1) >> tl) + 1 + ((a.S + r.tile - 1) >> tl);
+    const int all = ((s.ctx + s.len - 1) >> tl) + 1;
     w.tiles = most < all ? most : all;
     return w;
 }
@@ -80,12 +95,21 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
         }
         return;
     }
+    __shared__ ExtendSeq s_seq[NT];  // the block of sequences at hand
+    __shared__ Pair s_sums[NW];
+    __shared__ int s_at[NT];         // first unit of each
+    __shared__ int s_item[NT];       // first query tile
+    __shared__ unsigned s_v[NT];     // first key tile in the line
+    __shared__ unsigned s_tiles[NT]; // key tiles in the line of each of its query tiles
     // ---- rows of sequences at impossible positions
     for (int base = 0; base < a.N; base += NT) {
         const int n = base + (int)threadIdx.x;
-        if (!__syncthreads_or(n < a.N && extend_seq(a, n).bad)) continue;
-        for (int m = base; m < base + NT && m < a.N; ++m) {
-            const ExtendSeq s = extend_seq(a, m);
+        ExtendSeq mine{0, 0, 0, false};
+        if (n < a.N) mine = extend_seq(a, n);
+        s_seq[threadIdx.x] = mine;
+        if (!__syncthreads_or(mine.bad)) continue;
+        for (int m = 0; m < NT; ++m) {
+            const ExtendSeq s = s_seq[m];
             if (!s.bad) continue;
             const int64_t lo = (int64_t)s.row0 * a.H * a.d_v, n_o = (int64_t)s.len * a.H * a.d_v;
             for (int64_t i = threadIdx.x; i < n_o; i += NT) {
@@ -93,57 +117,61 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
                 else static_cast<unsigned*>(a.o)[lo + i] = 0x7fffffffu;
             }
         }
+        __syncthreads();
     }
-    // ---- the units of each route
-    __shared__ int s_sums[NW];
-    __shared__ int s_at[NT];     // first unit of each sequence of the block of sequences
-    __shared__ int s_item[NT];   // first query tile
-    __shared__ unsigned s_v[NT]; // first key tile in the line
+    // ---- the units of each route; s_seq has every sequence if they are one block
+    const bool one_block = a.N <= NT;
     for (int i = 0; i < 2; ++i) {
         const ExtendRoute& r = p.r[i];
         if (r.rows == 0) continue;
-        // the line of all key tiles; a length is halved until it fits 31 bits (a split is proportional)
-        int shift = 0, items = 0;
-        unsigned V = 0;
-        for (;;) {
-            long long v = 0;
-            int it = 0;
-            for (int n = threadIdx.x; n < a.N; n += NT) {
-                const SeqWork w = seq_work(a, p, i, extend_seq(a, n));
-                it += w.items;
-                v += (long long)w.items * ((w.tiles >> shift) + (shift > 0));
+        for (int x = threadIdx.x; x < r.cols * a.H; x += NT) r.count[x] = 0;
+        // this thread's sequence of a block: its query tiles and what each takes of the line
+        auto work_at = [&](int base, int shift, unsigned* t) {
+            const int n = base + (int)threadIdx.x;
+            SeqWork w{0, 0};
+            if (n < a.N) {
+                if (!one_block) s_seq[threadIdx.x] = extend_seq(a, n);
+                w = seq_work(a, p, i, s_seq[threadIdx.x]);
             }
-            int lo, hi;
-            block_incl(it, s_sums, &items);
-            block_incl((int)(v & 0xffff), s_sums, &lo);
-            block_incl((int)(v >> 16 < 0x3fffff ? v >> 16 : 0x3fffff), s_sums, &hi);
-            const long long all = ((long long)hi << 16) + lo;
-            V = (unsigned)all;
-            if (all < 0x7fffffff) break;
-            ++shift;
+            *t = w.items ? (unsigned)(w.tiles >> shift) + (shift > 0) : 0u;
+            return w;
+        };
+        // the line of all key tiles; lengths are halved until it fits 31 bits (a split is proportional)
+        int shift = 0;
+        unsigned t = 0;
+        SeqWork w{0, 0};
+        Pair at{0, 0}, tot{0, 0}, all;
+        for (;; ++shift) {
+            all = Pair{0, 0};
+            for (int base = 0; base < a.N; base += NT) {
+                w = work_at(base, shift, &t);
+                at = block_incl(Pair{w.items, (long long)w.items * t}, s_sums, &tot);
+                all.items += tot.items;
+                all.v += tot.v;
+            }
+            if (all.v < 0x7fffffff) break;
         }
+        const unsigned V = (unsigned)all.v;
         const unsigned even = (V + r.cols - 1) / r.cols;
         const unsigned Q = even > (unsigned)r.min_chunk ? even : r.min_chunk;
-        for (int x = threadIdx.x; x < r.cols * a.H; x += NT) r.count[x] = 0;
-        for (int c = threadIdx.x; c < r.cols; c += NT)
-            if (c * (unsigned long long)Q >= V) reinterpret_cast<int2*>(r.range)[c] = make_int2(1, 0);
         unsigned v_done = 0;
         int i_done = 0;
         for (int base = 0; base < a.N; base += NT) {
-            const int n = base + (int)threadIdx.x;
-            SeqWork w{0, 0};
-            if (n < a.N) w = seq_work(a, p, i, extend_seq(a, n));
-            const int t = w.items ? (w.tiles >> shift) + (shift > 0) : 0;
-            int tot_i, tot_v;
-            const int it = i_done + block_incl(w.items, s_sums, &tot_i) - w.items;
-            const unsigned v0 = v_done + (unsigned)(block_incl(w.items * t, s_sums, &tot_v) - w.items * t);
+            if (!one_block) {
+                w = work_at(base, shift, &t);
+                at = block_incl(Pair{w.items, (long long)w.items * t}, s_sums, &tot);
+            }
+            const int it = i_done + at.items - w.items;
+            const unsigned v0 = v_done + (unsigned)at.v - w.items * t;
             s_item[threadIdx.x] = it;
             s_v[threadIdx.x] = v0;
             s_at[threadIdx.x] = it + (int)(v0 / Q);
+            s_tiles[threadIdx.x] = t;
             __syncthreads();
+            const int last = min(NT, a.N - base) - 1;
             // the sequence of the block at a place of an array of firsts (ties: the last, which has items)
             auto find = [&](auto* first, auto x) {
-                int l = 0, h = NT - 1;
+                int l = 0, h = last;
                 while (l < h) {
                     const int m = (l + h + 1) >> 1;
                     if (first[m] <= x) l = m;
@@ -151,55 +179,51 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
                 }
                 return l;
             };
-            auto tiles_of = [&](int l) {
-                const SeqWork x = seq_work(a, p, i, extend_seq(a, base + l));
-                return (unsigned)((x.tiles >> shift) + (shift > 0));
-            };
-            if (tot_i > 0) {
-                const unsigned vb = v_done, ve = v_done + (unsigned)tot_v;
-                for (int c = threadIdx.x; c < r.cols; c += NT) {
-                    const unsigned long long b64 = (unsigned long long)c * Q;
-                    if (b64 >= V) break;
-                    const unsigned b = (unsigned)b64, e = (V - b > Q ? b + Q : V) - 1;
-                    if (b >= vb && b < ve) {
-                        const int l = find(s_v, b);
-                        r.range[2 * c] = s_item[l] + (int)((b - s_v[l]) / tiles_of(l));
-                    }
-                    if (e >= vb && e < ve) {
-                        const int l = find(s_v, e);
-                        r.range[2 * c + 1] = s_item[l] + (int)((e - s_v[l]) / tiles_of(l));
-                    }
+            const unsigned vb = v_done, ve = v_done + (unsigned)tot.v;
+            for (int c = threadIdx.x; c < r.cols; c += NT) {
+                const unsigned long long b64 = (unsigned long long)c * Q;
+                if (b64 >= V) {
+                    if (base == 0) reinterpret_cast<int2*>(r.range)[c] = make_int2(1, 0);
+                    continue;
                 }
-                const int id_end = i_done + tot_i - 1 + (int)((ve - 1) / Q);
-                for (int id = s_at[0] + (int)threadIdx.x; id <= id_end; id += NT) {
-                    const int l = find(s_at, id);
-                    const ExtendSeq sq = extend_seq(a, base + l);
-                    const SeqWork w2 = seq_work(a, p, i, sq);
-                    const unsigned t2 = (unsigned)((w2.tiles >> shift) + (shift > 0)), vs = s_v[l];
-                    if (w2.items == 0) continue;
-                    int lo = 0, hi = w2.items - 1;  // the query tile: the last whose first unit is at or before id
-                    while (lo < hi) {
-                        const int m = (lo + hi + 1) >> 1;
-                        if (s_item[l] + m + (int)((vs + m * t2) / Q) <= id) lo = m;
-                        else hi = m - 1;
-                    }
-                    const unsigned b = vs + lo * t2, e = b + t2 - 1, c = (unsigned)(id - s_item[l] - lo);
-                    const unsigned c0 = b / Q, c1 = e / Q;
-                    if (c < c0 || c > c1) continue;  // a cut between two tiles: no unit there
-                    const ExtendKeys k = extend_keys(sq, lo * r.rows, r.rows, r.tile, a.W, a.S);
-                    const unsigned x0 = c * Q > b ? c * Q - b : 0, x1 = e - b + 1 < (c + 1) * Q - b ? t2 : (c + 1) * Q - b;
-                    const int kt0 = (int)((unsigned long long)x0 * k.n / t2), kt1 = (int)((unsigned long long)x1 * k.n / t2);
-                    // parts of chunk x: 2 x for its first query tile, 2 x + 1 for a later one (its last)
-                    const int first = 2 * (int)c0 + (c0 * Q == b || c0 * Q > b ? 0 : 1);
-                    const bool split = c0 != c1;
-                    int4* to = reinterpret_cast<int4*>(r.units + id);
-                    to[0] = make_int4(base + l, lo * r.rows, kt0, kt1);
-                    to[1] = make_int4(split ? (c == c0 ? first : 2 * (int)c) : -1, split ? first : -1, (int)c0, (int)(c1 - c0 + 1));
-                    to[2] = make_int4(sq.row0, sq.len, sq.ctx, (int)c1);
+                const unsigned b = (unsigned)b64, e = (V - b > Q ? b + Q : V) - 1;
+                if (b >= vb && b < ve) {
+                    const int l = find(s_v, b);
+                    r.range[2 * c] = s_item[l] + (int)((b - s_v[l]) / s_tiles[l]);
+                }
+                if (e >= vb && e < ve) {
+                    const int l = find(s_v, e);
+                    r.range[2 * c + 1] = s_item[l] + (int)((e - s_v[l]) / s_tiles[l]);
                 }
             }
-            v_done += (unsigned)tot_v;
-            i_done += tot_i;
+            const int id_end = tot.items > 0 ? i_done + tot.items - 1 + (int)((ve - 1) / Q) : -1;
+            for (int id = s_at[0] + (int)threadIdx.x; id <= id_end; id += NT) {
+                const int l = find(s_at, id);
+                const ExtendSeq sq = s_seq[l];
+                const unsigned t2 = s_tiles[l], vs = s_v[l];
+                if (t2 == 0) continue;
+                int lo = 0, hi = ((sq.len + r.rows - 1) >> (__ffs(r.rows) - 1)) - 1;
+                while (lo < hi) {  // the query tile: the last whose first unit is at or before id
+                    const int m = (lo + hi + 1) >> 1;
+                    if (s_item[l] + m + (int)((vs + m * t2) / Q) <= id) lo = m;
+                    else hi = m - 1;
+                }
+                const unsigned b = vs + lo * t2, e = b + t2 - 1, c = (unsigned)(id - s_item[l] - lo);
+                const unsigned c0 = b / Q, c1 = e / Q;
+                if (c < c0 || c > c1) continue;  // a cut between two tiles: no unit there
+                const ExtendKeys k = extend_keys(sq, lo * r.rows, r.rows, r.tile, a.W, a.S);
+                const unsigned x0 = c * Q > b ? c * Q - b : 0, x1 = t2 < (c + 1) * Q - b ? t2 : (c + 1) * Q - b;
+                const int kt0 = (int)((unsigned long long)x0 * k.n / t2), kt1 = (int)((unsigned long long)x1 * k.n / t2);
+                // parts of chunk x: 2 x for its first query tile, 2 x + 1 for a later one (its last)
+                const int first = 2 * (int)c0 + (c0 * Q == b ? 0 : 1);
+                const bool split = c0 != c1;
+                int4* to = reinterpret_cast<int4*>(r.units + id);
+                to[0] = make_int4(base + l, lo * r.rows, kt0, kt1);
+                to[1] = make_int4(split ? (c == c0 ? first : 2 * (int)c) : -1, split ? first : -1, (int)c0, (int)(c1 - c0 + 1));
+                to[2] = make_int4(sq.row0, sq.len, sq.ctx, (int)c1);
+            }
+            v_done += (unsigned)tot.v;
+            i_done += tot.items;
             __syncthreads();
         }
     }

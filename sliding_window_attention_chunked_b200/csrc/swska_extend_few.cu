@@ -30,6 +30,7 @@ constexpr int HALF = KT * 128;             // bytes: KT rows x 64 columns
 constexpr int TILE = 2 * HALF;             // 8 KB: a key tile or one head's value tile
 constexpr int NTH = 32 * (kFewHeads + 1);
 constexpr int MAXST = 12;
+constexpr int kMaxParts = 8;               // parts of a query tile, in units of 32 (see cols below)
 constexpr int RING = 216 * 1024;
 constexpr int OFF_BAR = RING;
 constexpr int OFF_MASK = OFF_BAR + 2 * MAXST * 8;
@@ -317,27 +318,47 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
         __threadfence();
         for (int row = 0; row < rows; ++row) {
-            float M = -INFINITY;
-            for (int s = lane; s < u.nsplit; s += 32)
-                M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, h, row)].x));
+            // lane = part for the weights (as many as CTAs per head group, at most), lane = four columns for the sum
+            float M = -INFINITY, L = 0.f, mv[kMaxParts], w[kMaxParts];
+#pragma unroll
+            for (int i = 0; i < kMaxParts; ++i) {
+                const int s = lane + 32 * i;
+                const float2 ml = s < u.nsplit ? __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, h, row)]) : make_float2(-INFINITY, 0.f);
+                mv[i] = ml.x;
+                w[i] = ml.y;
+                M = fmaxf(M, ml.x);
+            }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
             const float base = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int s = 0; s < u.nsplit; ++s) {
-                const int64_t at = r.part_at(u.part_of(s), a.H, h, row);
-                const float2 ml = __ldcg(&r.part_ml[at]);
-                const float4 x4 = __ldcg(reinterpret_cast<const float4*>(r.part_o + at * HD) + lane);
-                const float w = tc::ex2(ml.x - base);
-                L = fmaf(ml.y, w, L);
-                O.x = fmaf(x4.x, w, O.x);
-                O.y = fmaf(x4.y, w, O.y);
-                O.z = fmaf(x4.z, w, O.z);
-                O.w = fmaf(x4.w, w, O.w);
+#pragma unroll
+            for (int i = 0; i < kMaxParts; ++i) {
+                mv[i] = tc::ex2(mv[i] - base);
+                L = fmaf(w[i], mv[i], L);
             }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
             const float inv = L == 0.f ? 0.f : 1.f / L;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kMaxParts; ++i) {
+                for (int s0 = 32 * i; s0 < min(32 * i + 32, u.nsplit); s0 += 16) {
+                    float4 x4[16];  // loads in flight together
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x4[e] = s0 + e < u.nsplit
+                                    ? __ldcg(reinterpret_cast<const float4*>(r.part_o + r.part_at(u.part_of(s0 + e), a.H, h, row) * HD) + lane)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float ws = __shfl_sync(0xffffffffu, mv[i], (s0 + e) & 31);
+                        O.x = fmaf(x4[e].x, ws, O.x);
+                        O.y = fmaf(x4[e].y, ws, O.y);
+                        O.z = fmaf(x4[e].z, ws, O.z);
+                        O.w = fmaf(x4[e].w, ws, O.w);
+                    }
+                }
+            }
             store4(out + ((row0 + row) * a.H + h) * HD + 4 * lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
         }
     }
@@ -346,6 +367,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }  // namespace
 
 cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, cudaStream_t s) {
+    if (r.cols > 32 * kMaxParts) return cudaErrorInvalidConfiguration;
     const int hpg = (a.H + r.groups - 1) / r.groups;
     int box = KT;
     while (a.page % box != 0) box /= 2;

@@ -448,31 +448,47 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!wait_bar_warp(&meet[h], (uint32_t)(meets++ & 1), abort_flag)) { ok = false; break; }
             if (!came_last[h]) continue;
             __threadfence();
-            for (int rr = warp % 4; rr < rows; rr += 4) {
-                float M = -INFINITY;
-                for (int s = lane; s < u.nsplit; s += 32)
-                    M = fmaxf(M, __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, hd, rr)].x));
+            // this warp adds its 32 rows: lane = row for the weights, lane = four columns for the sums, eight
+            // rows at a time so that their loads are in flight together
+            float M = -INFINITY, Lsum = 0.f;
+            const bool in = row < rows;
+            for (int s = 0; s < u.nsplit; ++s) {
+                const float2 ml = in ? __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, hd, row)]) : make_float2(-INFINITY, 0.f);
+                const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
+                Lsum = fmaf(ml.y, tc::ex2(ml.x - base), Lsum * tc::ex2(M - base));
+                M = mn;
+            }
+            const float base = M == -INFINITY ? 0.f : M, iv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+            const int w0 = 32 * (warp % 4);  // the warp's first row
+            for (int r0 = 0; r0 < 32 && w0 + r0 < rows; r0 += 8) {
+                float4 O[8];
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                const float base = M == -INFINITY ? 0.f : M;
-                float Lsum = 0.f;
-                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+                for (int i = 0; i < 8; ++i) O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
                 for (int s = 0; s < u.nsplit; ++s) {
-                    const int64_t pa = r.part_at(u.part_of(s), a.H, hd, rr);
-                    const float2 ml = __ldcg(&r.part_ml[pa]);
-                    if (ml.x == -INFINITY) continue;  // nothing seen there; an empty part holds no output
-                    const float4 x4 = __ldcg(reinterpret_cast<const float4*>(r.part_o + pa * HD) + lane);
-                    const float w = tc::ex2(ml.x - base);
-                    Lsum = fmaf(ml.y, w, Lsum);
-                    O.x = fmaf(x4.x, w, O.x);
-                    O.y = fmaf(x4.y, w, O.y);
-                    O.z = fmaf(x4.z, w, O.z);
-                    O.w = fmaf(x4.w, w, O.w);
+                    const int part = u.part_of(s);
+                    float w = 0.f;
+                    if (in) w = tc::ex2(__ldcg(&r.part_ml[r.part_at(part, a.H, hd, row)].x) - base) * iv;
+                    float4 x4[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x4[i] = w0 + r0 + i < rows
+                                    ? __ldcg(reinterpret_cast<const float4*>(r.part_o + r.part_at(part, a.H, hd, w0 + r0 + i) * HD) + lane)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float wi = __shfl_sync(0xffffffffu, w, r0 + i);
+                        if (wi == 0.f) continue;  // nothing seen there: an empty part holds no output
+                        O[i].x = fmaf(x4[i].x, wi, O[i].x);
+                        O[i].y = fmaf(x4[i].y, wi, O[i].y);
+                        O[i].z = fmaf(x4[i].z, wi, O[i].z);
+                        O[i].w = fmaf(x4[i].w, wi, O[i].w);
+                    }
                 }
-                const float iv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-                store4(static_cast<__nv_bfloat16*>(a.o) + ((int64_t)(u.row0 + u.q0 + rr) * a.H + hd) * HD + 4 * lane,
-                       make_float4(O.x * iv, O.y * iv, O.z * iv, O.w * iv));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (w0 + r0 + i < rows)
+                        store4(static_cast<__nv_bfloat16*>(a.o) + ((int64_t)(u.row0 + u.q0 + w0 + r0 + i) * a.H + hd) * HD + 4 * lane, O[i]);
             }
         }
     }

@@ -46,20 +46,9 @@ __device__ __forceinline__ long long warp_incl(long long x, int lane) {
     return x;
 }
 
-// Inclusive scan of one value per thread over the block; every thread also gets the block's sum.
-__device__ long long block_incl(long long x, long long* warp_sums, long long* total) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    x = warp_incl(x, lane);
-    __syncthreads();  // the previous use of warp_sums is over
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        const long long w = warp_incl(lane < NW ? warp_sums[lane] : 0, lane);
-        if (lane < NW) warp_sums[lane] = w;
-    }
-    __syncthreads();
-    if (warp > 0) x += warp_sums[warp - 1];
-    *total = warp_sums[NW - 1];
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
 
@@ -75,33 +64,57 @@ struct TableArgs {
     int N, max_pages, P, page, W, S, M;
 };
 
-// what one sequence gives back and wants; pages are counted by the warp that owns the sequence
+// what one sequence gives back and wants, as logical pages. Positions are clamped to 2^31, past any
+// row of the table (max_pages * page is below), so that the divisions are 32-bit ones.
 struct Range {
-    int rel_lo, rel_hi;  // logical pages that may go back
-    int want_lo, want_hi;
-    bool active, done, fits;
-    int low;
+    int rel_lo, rel_hi;    // pages that may go back
+    int want_lo, want_hi;  // pages of the new tokens
+    int first;             // new value of first
+    int tokens;            // wanted; -1: the row has no room for them, -2: finished (walked by the whole CTA)
 };
-__device__ __forceinline__ Range range_of(const TableArgs& a, int n) {
-    Range r;
-    const int64_t c = a.ctx[n];
-    const int m = a.n_new[n];
+__device__ __forceinline__ Range range_of(const TableArgs& a, int64_t c, int m, int f) {
+    Range r{0, 0, 0, 0, f, 0};
+    if (c < 0 || m == 0) return r;
+    if (m < 0) {
+        r.rel_hi = a.max_pages;
+        r.first = 0;
+        return r;
+    }
+    const unsigned page = (unsigned)a.page, cap = 1u << 31;
+    c = c < (1ll << 32) ? c : (1ll << 32);
+    auto clamp = [&](int64_t x) { return x < 0 ? 0u : (x < (int64_t)cap ? (unsigned)x : cap); };
     const int sp = (a.S + a.page - 1) / a.page;
-    r.active = m > 0 && c >= 0;
-    r.done = m < 0 && c >= 0;
-    const int64_t used = (c + a.page - 1) / a.page, end = (c + (m > 0 ? m : 0) + a.page - 1) / a.page;
-    int64_t low = (c - a.W + 1 > 0 ? c - a.W + 1 : 0) / a.page;
-    low = low > sp ? low : sp;
+    const unsigned used = clamp(c) / page + (clamp(c) % page != 0);
+    const unsigned end = clamp(c + m) / page + (clamp(c + m) % page != 0);
+    unsigned low = clamp(c - a.W + 1) / page;
+    low = low > (unsigned)sp ? low : (unsigned)sp;
     low = low < used ? low : used;
-    low = low < a.max_pages ? low : a.max_pages;
-    const int f = a.first[n];
-    r.low = (int)low;
-    r.rel_lo = r.done ? 0 : (f > sp ? f : sp);
-    r.rel_hi = r.done ? a.max_pages : (r.active ? (int)low : 0);
-    r.fits = r.active && end <= a.max_pages;
-    r.want_lo = r.fits ? (int)used : 0;
-    r.want_hi = r.fits ? (int)end : 0;
+    low = low < (unsigned)a.max_pages ? low : (unsigned)a.max_pages;
+    r.rel_lo = f > sp ? f : sp;
+    r.rel_hi = (int)low;
+    r.first = f > (int)low ? f : (int)low;
+    const bool fits = end <= (unsigned)a.max_pages;
+    r.want_lo = fits ? (int)used : 0;
+    r.want_hi = fits ? (int)end : 0;
+    r.tokens = fits ? m : -1;
     return r;
+}
+
+// entries of a row in [lo, hi) through the warp, UN x 32 at a time so that their loads overlap; take(p,
+// e) gets each lane's entry (-1 outside the range)
+template <int UN, typename F>
+__device__ __forceinline__ void walk(const int32_t* row, int lo, int hi, int lane, F take) {
+    for (int p0 = lo; p0 < hi; p0 += 32 * UN) {
+        int32_t e[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int p = p0 + 32 * i + lane;
+            e[i] = p < hi ? __ldcg(row + p) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+            if (p0 + 32 * i < hi) take(p0 + 32 * i + lane, e[i]);
+    }
 }
 
 __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
@@ -112,51 +125,82 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
     const int n0 = min(a.N, rank * per), n1 = min(a.N, n0 + per);
 
     extern __shared__ int32_t sh[];
-    // own sequences: pages back, pages wanted, and the ranks where they start; all sequences: cu
-    int32_t* s_rel = sh;
+    // own sequences: their ranges, pages back and wanted, and the ranks where these start; then all
+    // sequences' cu and positions
+    Range* s_range = reinterpret_cast<Range*>(sh);
+    int32_t* s_rel = sh + 6 * per;
     int32_t* s_need = s_rel + per;
     int32_t* s_relat = s_need + per;
     int32_t* s_takeat = s_relat + per;  // -1: not served
     int32_t* s_cu = s_takeat + per;     // [N + 1]
-    __shared__ long long warp_sums[NW];
+    int32_t* s_ctx = s_cu + a.N + 1;    // [N]
     __shared__ Sums s_tot;              // this CTA's sums of the first exchange
     __shared__ long long s_tot2[2];     // pages taken and tokens served, of the second
+    __shared__ int s_done[NT];          // finished sequences of this CTA, while they fit
+    __shared__ int s_ndone;
+    __shared__ int s_held[NW];
 
     int count0 = *a.free_count;
     count0 = count0 < 0 ? 0 : (count0 > a.P ? a.P : count0);
     const unsigned P = (unsigned)a.P;
+    const int mine = n1 - n0;
 
+    if (threadIdx.x == 0) s_ndone = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < mine; i += NT) {
+        const int m = a.n_new[n0 + i];
+        s_range[i] = range_of(a, a.ctx[n0 + i], m, a.first[n0 + i]);
+        s_rel[i] = s_need[i] = 0;
+        // a finished row is walked to its end: by all warps together (past NT of them, by one)
+        if (s_range[i].rel_hi == a.max_pages && m < 0) {
+            const int d = atomicAdd(&s_ndone, 1);
+            if (d < NT) {
+                s_done[d] = i;
+                s_range[i].tokens = -2;
+            }
+        }
+    }
+    // positions of the slot map: a served one is below 2^31
+    for (int n = threadIdx.x; n < a.N; n += NT) s_ctx[n] = (int32_t)a.ctx[n];
+    __syncthreads();
+    const int n_done = min(s_ndone, NT);
     // ---- counts: a warp per sequence
-    for (int n = n0 + warp; n < n1; n += NW) {
-        const Range r = range_of(a, n);
-        const int32_t* row = a.table + (int64_t)n * a.max_pages;
+    for (int i = warp; i < mine; i += NW) {
+        const Range r = s_range[i];
+        if (r.tokens == -2) continue;
+        const int32_t* row = a.table + (int64_t)(n0 + i) * a.max_pages;
         int rel = 0, need = 0;
-        for (int p = r.rel_lo + lane; p < r.rel_hi; p += 32) rel += (unsigned)row[p] < P;
-        for (int p = r.want_lo + lane; p < r.want_hi; p += 32) need += (unsigned)row[p] >= P;
+        walk<4>(row, r.rel_lo, r.rel_hi, lane, [&](int, int32_t e) { rel += (unsigned)e < P; });
+        walk<4>(row, r.want_lo, r.want_hi, lane, [&](int p, int32_t e) { need += p < r.want_hi && (unsigned)e >= P; });
         rel = __reduce_add_sync(0xffffffffu, rel);
         need = __reduce_add_sync(0xffffffffu, need);
         if (lane == 0) {
-            s_rel[n - n0] = rel;
-            s_need[n - n0] = need;
+            s_rel[i] = rel;
+            s_need[i] = need;
         }
     }
+    for (int d = 0; d < n_done; ++d) {
+        const int32_t* row = a.table + (int64_t)(n0 + s_done[d]) * a.max_pages;
+        int rel = 0;
+#pragma unroll 4
+        for (int p = threadIdx.x; p < a.max_pages; p += NT) rel += (unsigned)__ldcg(row + p) < P;
+        rel = __reduce_add_sync(0xffffffffu, rel);
+        if (lane == 0 && rel > 0) atomicAdd(&s_rel[s_done[d]], rel);
+    }
     __syncthreads();
-    // ---- this CTA's sums
-    {
+    // ---- this CTA's sums (tokens wanted count whether or not they fit)
+    if (warp == 0) {
         Sums t{0, 0, 0};
-        for (int i = threadIdx.x; i < n1 - n0; i += NT) {
-            const int m = a.n_new[n0 + i];
+        for (int i = lane; i < mine; i += 32) {
+            const int tokens = s_range[i].tokens;
             t.rel += s_rel[i];
             t.need += s_need[i];
-            t.tok += (m > 0 && a.ctx[n0 + i] >= 0) ? m : 0;
+            t.tok += tokens == 0 || tokens == -2 ? 0 : a.n_new[n0 + i];
         }
-        long long all;
-        block_incl(t.rel, warp_sums, &all);
-        if (threadIdx.x == 0) s_tot.rel = all;
-        block_incl(t.need, warp_sums, &all);
-        if (threadIdx.x == 0) s_tot.need = all;
-        block_incl(t.tok, warp_sums, &all);
-        if (threadIdx.x == 0) s_tot.tok = all;
+        t.rel = warp_sum(t.rel);
+        t.need = warp_sum(t.need);
+        t.tok = warp_sum(t.tok);
+        if (lane == 0) s_tot = t;
     }
     cluster.sync();
     Sums before{0, 0, 0};
@@ -173,61 +217,81 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
     const long long avail = (long long)count0 + R;
 
     // ---- which sequences are served, and the ranks inside this CTA
-    long long run_rel = 0, run_need = 0, run_tok = 0, run_take = 0, run_served = 0;
-    for (int base = 0; base < n1 - n0; base += NT) {
-        const int i = base + (int)threadIdx.x;
-        const bool in = i < n1 - n0;
-        const int n = n0 + i;
-        const int m = in ? a.n_new[n] : 0;
-        const bool active = in && m > 0 && a.ctx[n] >= 0;
-        const int rel = in ? s_rel[i] : 0, need = in ? s_need[i] : 0;
-        long long tot_rel, tot_need, tot_tok, tot_take, tot_served;
-        const long long at_rel = block_incl(rel, warp_sums, &tot_rel);
-        const long long at_need = block_incl(need, warp_sums, &tot_need);
-        const long long at_tok = block_incl(active ? m : 0, warp_sums, &tot_tok);
-        bool ok = false;
-        if (active)
-            ok = range_of(a, n).fits && before.tok + run_tok + at_tok <= a.M &&
-                 (need == 0 || before.need + run_need + at_need <= avail);
-        const long long at_take = block_incl(ok ? need : 0, warp_sums, &tot_take);
-        const long long at_served = block_incl(ok ? m : 0, warp_sums, &tot_served);
-        if (in) {
-            s_relat[i] = (int)(run_rel + at_rel - rel);
-            s_takeat[i] = ok ? (int)(run_take + at_take - need) : -1;
-            s_cu[n + 1] = (int)(run_served + at_served);  // relative to this CTA until the second exchange
+    if (warp == 0) {
+        long long run_rel = 0, run_need = before.need, run_tok = before.tok, run_take = 0, run_served = 0;
+        for (int base = 0; base < mine; base += 32) {
+            const int i = base + lane;
+            const bool in = i < mine;
+            const int tokens = in ? s_range[i].tokens : 0;
+            const int m = tokens == 0 || tokens == -2 ? 0 : a.n_new[n0 + i];
+            const int rel = in ? s_rel[i] : 0, need = in ? s_need[i] : 0;
+            const long long at_rel = run_rel + warp_incl(rel, lane), at_need = run_need + warp_incl(need, lane),
+                            at_tok = run_tok + warp_incl(m, lane);
+            const bool ok = tokens > 0 && at_tok <= a.M && (need == 0 || at_need <= avail);
+            const long long at_take = run_take + warp_incl(ok ? need : 0, lane);
+            const long long at_served = run_served + warp_incl(ok ? m : 0, lane);
+            if (in) {
+                s_relat[i] = (int)(at_rel - rel);
+                s_takeat[i] = ok ? (int)(at_take - need) : -1;
+                s_cu[n0 + i + 1] = (int)at_served;  // relative to this CTA until the second exchange
+            }
+            run_rel = __shfl_sync(0xffffffffu, at_rel, 31);
+            run_need = __shfl_sync(0xffffffffu, at_need, 31);
+            run_tok = __shfl_sync(0xffffffffu, at_tok, 31);
+            run_take = __shfl_sync(0xffffffffu, at_take, 31);
+            run_served = __shfl_sync(0xffffffffu, at_served, 31);
         }
-        run_rel += tot_rel;
-        run_need += tot_need;
-        run_tok += tot_tok;
-        run_take += tot_take;
-        run_served += tot_served;
-    }
-    if (threadIdx.x == 0) {
-        s_tot2[0] = run_take;
-        s_tot2[1] = run_served;
+        if (lane == 0) {
+            s_tot2[0] = run_take;
+            s_tot2[1] = run_served;
+        }
     }
     __syncthreads();
     // ---- pages back: onto the stack
-    for (int n = n0 + warp; n < n1; n += NW) {
-        const Range r = range_of(a, n);
-        int32_t* row = a.table + (int64_t)n * a.max_pages;
-        long long at = count0 + before.rel + s_relat[n - n0];
-        __syncwarp();
-        for (int p0 = r.rel_lo; p0 < r.rel_hi; p0 += 32) {
-            const int p = p0 + lane;
-            const int32_t e = p < r.rel_hi ? row[p] : -1;
+    for (int i = warp; i < mine; i += NW) {
+        const Range r = s_range[i];
+        if (r.tokens == -2) continue;
+        int32_t* row = a.table + (int64_t)(n0 + i) * a.max_pages;
+        long long at = count0 + before.rel + s_relat[i];
+        walk<4>(row, r.rel_lo, r.rel_hi, lane, [&](int p, int32_t e) {
             const bool held = (unsigned)e < P;
             const unsigned who = __ballot_sync(0xffffffffu, held);
             const long long to = at + __popc(who & ((1u << lane) - 1u));
             if (held && to < a.P) a.free_list[to] = e;
-            if (p < r.rel_hi) row[p] = -1;
+            if (e != -1) row[p] = -1;
             at += __popc(who);
-        }
-        if (lane == 0) {
-            if (r.done) a.first[n] = 0;
-            else if (r.active && a.first[n] < r.low) a.first[n] = r.low;
+        });
+    }
+    for (int d = 0; d < n_done; ++d) {
+        int32_t* row = a.table + (int64_t)(n0 + s_done[d]) * a.max_pages;
+        long long at = count0 + before.rel + s_relat[s_done[d]];
+        for (int p0 = 0; p0 < a.max_pages; p0 += 4 * NT) {
+            int32_t e[4];
+            bool some = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = p0 + k * NT + (int)threadIdx.x;
+                e[k] = p < a.max_pages ? __ldcg(row + p) : -1;
+                some = some || e[k] != -1;
+            }
+            if (!__syncthreads_or(some)) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool held = (unsigned)e[k] < P;
+                const unsigned who = __ballot_sync(0xffffffffu, held);
+                if (lane == 0) s_held[warp] = __popc(who);
+                __syncthreads();
+                const int c = s_held[lane];
+                const int before_me = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+                const long long to = at + before_me + __popc(who & ((1u << lane) - 1u));
+                if (held && to < a.P) a.free_list[to] = e[k];
+                if (e[k] != -1) row[p0 + k * NT + (int)threadIdx.x] = -1;
+                at += __reduce_add_sync(0xffffffffu, c);
+                __syncthreads();
+            }
         }
     }
+    for (int i = threadIdx.x; i < mine; i += NT) a.first[n0 + i] = s_range[i].first;
     // stack entries written by the other CTAs are visible after this barrier
     cluster.sync();
     long long take0 = 0, served0 = 0, A = 0, total = 0;
@@ -242,22 +306,21 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
     }
     const long long top = avail < a.P ? avail : a.P;
     // ---- pages wanted: off the stack
-    for (int n = n0 + warp; n < n1; n += NW) {
-        const int takeat = s_takeat[n - n0];
-        if (takeat < 0) continue;  // the whole warp
-        const Range r = range_of(a, n);
-        int32_t* row = a.table + (int64_t)n * a.max_pages;
+    for (int i = warp; i < mine; i += NW) {
+        const int takeat = s_takeat[i];
+        if (takeat < 0 || s_need[i] == 0) continue;  // the whole warp
+        const Range r = s_range[i];
+        int32_t* row = a.table + (int64_t)(n0 + i) * a.max_pages;
         long long j = take0 + takeat;
-        for (int p0 = r.want_lo; p0 < r.want_hi; p0 += 32) {
-            const int p = p0 + lane;
-            const bool lack = p < r.want_hi && (unsigned)row[p] >= P;
+        walk<4>(row, r.want_lo, r.want_hi, lane, [&](int p, int32_t e) {
+            const bool lack = p < r.want_hi && (unsigned)e >= P;
             const unsigned who = __ballot_sync(0xffffffffu, lack);
             const long long from = top - 1 - (j + __popc(who & ((1u << lane) - 1u)));
             if (lack) row[p] = from >= 0 ? __ldcg(a.free_list + from) : -1;
             j += __popc(who);
-        }
+        });
     }
-    for (int i = threadIdx.x; i < n1 - n0; i += NT) a.cu[n0 + i + 1] = (int)(served0 + s_cu[n0 + i + 1]);
+    for (int i = threadIdx.x; i < mine; i += NT) a.cu[n0 + i + 1] = (int)(served0 + s_cu[n0 + i + 1]);
     if (rank == 0 && threadIdx.x == 0) {
         a.cu[0] = 0;
         *a.free_count = (int)(top - A > 0 ? top - A : 0);
@@ -285,7 +348,7 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
                 const int i = i0 + u;
                 if (i >= total) break;
                 while (s_cu[n + 1] <= i) ++n;  // past sequences without tokens too
-                const unsigned pos = (unsigned)(a.ctx[n] + (i - s_cu[n]));
+                const unsigned pos = (unsigned)s_ctx[n] + (unsigned)(i - s_cu[n]);
                 const int p = (int)(pos / (unsigned)a.page);
                 if (n != seen_n || p != seen_p) {
                     e = __ldcg(a.table + (int64_t)n * a.max_pages + p);
@@ -313,7 +376,7 @@ cudaError_t swska_page_tables_launch(const int64_t* ctx, const int32_t* n_new, i
     // than that takes the largest portable cluster
     const int CL = N <= NW && M <= 4 * NT ? 1 : kClusterMax;
     const int per = (N + CL - 1) / CL;
-    const size_t smem = ((size_t)4 * per + N + 1) * sizeof(int32_t);
+    const size_t smem = ((size_t)10 * per + 2 * (size_t)N + 1) * sizeof(int32_t);
     cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
