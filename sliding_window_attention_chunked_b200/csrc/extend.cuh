@@ -32,6 +32,7 @@ struct ExtendRoute {
     int groups = 1;          // head groups
     int cols = 1;            // CTAs per head group
     int min_chunk = 1;       // key tiles that a CTA takes at least
+    int split_cost = 0;      // what the parts of a cut query tile cost, in key tiles
     int part_rows = 0;       // rows kept of a part
     int cap_items = 0;
     ExtendUnit* units = nullptr;  // [cap_items + cols]: unit of query tile i in chunk c at i + c

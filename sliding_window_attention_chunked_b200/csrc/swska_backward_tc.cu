@@ -116,6 +116,11 @@ using fx::f2add;
 using fx::f2fma;
 using fx::f2mul;
 using fx::f2sub;
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float2 raw2(const uint32_t* r, int e) {
     return make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
 }
@@ -172,9 +177,9 @@ __device__ __forceinline__ uint32_t packed_col(int k) { return (uint32_t)(8 * k 
 // There D = dbuf comes from the stored bf16 o, off by about 2^-9 of it. Where a row's attention is
 // peaked, dS = p (dP - D) of the peak is a small difference and that error would show. So the sweep
 // also sums e = sum_j p_j (dP_j - D) of each row in fp32, D + e (the row's own sum p dP) goes back to
-// dbuf for the key-tile kernel, and a CTA with a peaked row (sum of p^2 over half the columns above
-// 1/8, so above 1/4 in all) sweeps its tiles once more with it. Rows that see few keys always are
-// (the first tile, short windows: a sweep of few tiles); for long windows only peaked ones are.
+// dbuf for the key-tile kernel, and a CTA with a row that has some p above 1/2 sweeps its tiles once
+// more with it. Rows that see few keys are such rows (the first tile, short windows: a sweep of few
+// tiles); with long windows only peaked ones are.
 template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -367,7 +372,8 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         float Dr = dbuf[(int64_t)bh * Tpad + t];
         const float2 sl2 = make_float2(scale_log2, scale_log2), nl2 = make_float2(nL, nL);
         float2 d2 = make_float2(Dr, Dr);
-        float2 e2 = make_float2(0.f, 0.f), pp2 = make_float2(0.f, 0.f);  // SINK: sums of dS and p^2
+        float2 e2 = make_float2(0.f, 0.f);  // SINK: sum of dS
+        float p_max = 0.f;                  // SINK: the largest p
         bool ok = true;
         int u_end = n_it;
         bool met = false;  // SINK: the softmax warps' meeting after the first sweep
@@ -415,7 +421,7 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     pk[i] = pack_bf16x2(ds.x, ds.y);
                     if (SINK) {
                         e2 = f2add(e2, ds);
-                        pp2 = f2fma(p2[16 * c + i], p2[16 * c + i], pp2);
+                        p_max = fmax3(p_max, p2[16 * c + i].x, p2[16 * c + i].y);
                     }
                 }
                 tc::tmem_st16(tS + 16u * c, pk);
@@ -426,7 +432,7 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (SINK && u == n_it - 1) {
                 float* sums = reinterpret_cast<float*>(smem + OFF_SUMS);
                 sums[TILE * w + row] = e2.x + e2.y;
-                if (t < T && pp2.x + pp2.y > 0.125f) *redo = 1;
+                if (t < T && p_max > 0.5f) *redo = 1;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 met = true;
                 Dr += sums[row] + sums[TILE + row];

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
     __shared__ int s_at[NT];         // first unit of each
     __shared__ int s_item[NT];       // first query tile
     __shared__ unsigned s_v[NT];     // first key tile in the line
+    __shared__ unsigned s_most;
     __shared__ unsigned s_tiles[NT]; // key tiles in the line of each of its query tiles
     // ---- rows of sequences at impossible positions
     for (int base = 0; base < a.N; base += NT) {
@@ -151,15 +152,35 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
             }
             if (all.v < 0x7fffffff) break;
         }
-        const unsigned V = (unsigned)all.v;
-        const unsigned even = (V + r.cols - 1) / r.cols;
-        const unsigned Q = even > (unsigned)r.min_chunk ? even : r.min_chunk;
+        // Even chunks cost r.split_cost key tiles more (parts to write and add). Whole query tiles, dealt
+        // out with the longest one's room for each, are taken where that is less.
+        if (threadIdx.x == 0) s_most = 0;
+        __syncthreads();
+        for (int base = 0; base < a.N; base += NT) {
+            if (!one_block) work_at(base, shift, &t);
+            if (t > 0) atomicMax(&s_most, t);
+        }
+        __syncthreads();
+        const unsigned t_max = s_most;
+        unsigned V = (unsigned)all.v;
+        const unsigned even = (V + r.cols - 1) / r.cols, rounds = ((unsigned)all.items + r.cols - 1) / r.cols;
+        unsigned Q = even > (unsigned)r.min_chunk ? even : r.min_chunk;
+        const bool whole = (unsigned long long)rounds * t_max <= (unsigned long long)Q + r.split_cost;
+        if (whole) {
+            Q = rounds * t_max;
+            V = (unsigned)all.items * t_max;
+        }
         unsigned v_done = 0;
         int i_done = 0;
         for (int base = 0; base < a.N; base += NT) {
             if (!one_block) {
                 w = work_at(base, shift, &t);
                 at = block_incl(Pair{w.items, (long long)w.items * t}, s_sums, &tot);
+            }
+            if (whole) {
+                t = w.items ? t_max : 0;
+                at.v = (long long)at.items * t_max;
+                tot.v = (long long)tot.items * t_max;
             }
             const int it = i_done + at.items - w.items;
             const unsigned v0 = v_done + (unsigned)at.v - w.items * t;
@@ -237,7 +258,8 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
     ExtendPlan p;
     if (max_len > M) max_len = M;
     // ctas: what the GPU holds at once
-    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int64_t items) {
+    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int split_cost,
+                     int64_t items) {
         ExtendRoute& r = p.r[i];
         r.rows = rows;
         r.part_rows = part_rows;
@@ -245,20 +267,21 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         r.groups = groups;
         r.cols = ctas / groups > 1 ? ctas / groups : 1;
         r.min_chunk = min_chunk;
+        r.split_cost = split_cost;
         r.cap_items = (int)(items < M ? items : M);
     };
     const int sms = device_sm_count();
     if (bf16 && dk == 128 && dv == 128) {
         const int few = max_len < kFewRows ? max_len : kFewRows;
-        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 2, N);
+        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 4, 6, N);
         p.short_len = kFewRows;
         if (max_len > kFewRows)
-            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, (int64_t)M / kChunkRows + N);
+            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 6, (int64_t)M / kChunkRows + N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
     const int rows = max_len <= 16 ? 16 : 64;
-    route(0, rows, rows, 64, H, (rows == 16 ? 4 : 2) * sms, 1, (int64_t)M / rows + N);
+    route(0, rows, rows, 64, H, (rows == 16 ? 4 : 2) * sms, 1, 1, (int64_t)M / rows + N);
     return p;
 }
 

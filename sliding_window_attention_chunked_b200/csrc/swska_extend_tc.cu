@@ -406,6 +406,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int hd = head[h];
             __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + ((int64_t)(u.row0 + u.q0 + row) * a.H + hd) * HD;
             const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            // this row's four columns of group c in a part
+            auto part_col = [&](int part, int hdx, int c) {
+                return r.part_o + r.part_at(part, a.H, hdx, 0) * HD + ((int64_t)c * BM + row) * 4;
+            };
             const int64_t at = u.part >= 0 ? r.part_at(u.part, a.H, hd, row) : 0;
             if (n_it > 0) {
 #pragma unroll
@@ -424,9 +428,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             *reinterpret_cast<uint4*>(orow + cb + i) = w;
                         }
                     } else if (live) {
+                        // a part's rows are stored column group by column group: neighbouring threads write
+                        // neighbouring 16 bytes
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4*>(r.part_o + at * HD + cb + i) = make_uint4(t[i], t[i + 1], t[i + 2], t[i + 3]);
+                            *reinterpret_cast<uint4*>(part_col(u.part, hd, (cb + i) / 4)) = make_uint4(t[i], t[i + 1], t[i + 2], t[i + 3]);
                     }
                 }
                 Lb += 3 * n_it;
@@ -448,47 +454,47 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!wait_bar_warp(&meet[h], (uint32_t)(meets++ & 1), abort_flag)) { ok = false; break; }
             if (!came_last[h]) continue;
             __threadfence();
-            // this warp adds its 32 rows: lane = row for the weights, lane = four columns for the sums, eight
-            // rows at a time so that their loads are in flight together
+            // every thread adds its row: the maximum and sum first, then 32 columns at a time
+            if (row >= rows) continue;
             float M = -INFINITY, Lsum = 0.f;
-            const bool in = row < rows;
+#pragma unroll 4
             for (int s = 0; s < u.nsplit; ++s) {
-                const float2 ml = in ? __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, hd, row)]) : make_float2(-INFINITY, 0.f);
+                const float2 ml = __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, hd, row)]);
                 const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
                 Lsum = fmaf(ml.y, tc::ex2(ml.x - base), Lsum * tc::ex2(M - base));
                 M = mn;
             }
             const float base = M == -INFINITY ? 0.f : M, iv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-            const int w0 = 32 * (warp % 4);  // the warp's first row
-            for (int r0 = 0; r0 < 32 && w0 + r0 < rows; r0 += 8) {
+            for (int cb = 0; cb < HD; cb += 32) {
                 float4 O[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int s = 0; s < u.nsplit; ++s) {
                     const int part = u.part_of(s);
-                    float w = 0.f;
-                    if (in) w = tc::ex2(__ldcg(&r.part_ml[r.part_at(part, a.H, hd, row)].x) - base) * iv;
+                    const float m = __ldcg(&r.part_ml[r.part_at(part, a.H, hd, row)].x);
                     float4 x4[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x4[i] = w0 + r0 + i < rows
-                                    ? __ldcg(reinterpret_cast<const float4*>(r.part_o + r.part_at(part, a.H, hd, w0 + r0 + i) * HD) + lane)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i = 0; i < 8; ++i) x4[i] = __ldcg(reinterpret_cast<const float4*>(part_col(part, hd, cb / 4 + i)));
+                    if (m == -INFINITY) continue;  // nothing seen there; an empty part holds no output
+                    const float w = tc::ex2(m - base) * iv;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float wi = __shfl_sync(0xffffffffu, w, r0 + i);
-                        if (wi == 0.f) continue;  // nothing seen there: an empty part holds no output
-                        O[i].x = fmaf(x4[i].x, wi, O[i].x);
-                        O[i].y = fmaf(x4[i].y, wi, O[i].y);
-                        O[i].z = fmaf(x4[i].z, wi, O[i].z);
-                        O[i].w = fmaf(x4[i].w, wi, O[i].w);
+                        O[i].x = fmaf(x4[i].x, w, O[i].x);
+                        O[i].y = fmaf(x4[i].y, w, O[i].y);
+                        O[i].z = fmaf(x4[i].z, w, O[i].z);
+                        O[i].w = fmaf(x4[i].w, w, O[i].w);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (w0 + r0 + i < rows)
-                        store4(static_cast<__nv_bfloat16*>(a.o) + ((int64_t)(u.row0 + u.q0 + w0 + r0 + i) * a.H + hd) * HD + 4 * lane, O[i]);
+                for (int i = 0; i < 8; i += 2) {
+                    uint4 wv;
+                    wv.x = pack_bf16x2(O[i].x, O[i].y);
+                    wv.y = pack_bf16x2(O[i].z, O[i].w);
+                    wv.z = pack_bf16x2(O[i + 1].x, O[i + 1].y);
+                    wv.w = pack_bf16x2(O[i + 1].z, O[i + 1].w);
+                    *reinterpret_cast<uint4*>(orow + cb + 4 * i) = wv;
+                }
             }
         }
     }
