@@ -61,9 +61,10 @@ cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, bool fp32, uint64_t
                          uint64_t d2, uint32_t box0, uint32_t box1, bool swizzle128);
 cudaError_t make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
                               uint64_t d2, uint32_t box0, uint32_t box1);
-// the same with the byte strides of dimensions 1 and 2 given (multiples of 16)
+// the same with the byte strides of dimensions 1 and 2 given (multiples of 16), and boxes of box2 matrices
 cudaError_t make_tmap_bf16_3d_strided(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                                      uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1);
+                                      uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1,
+                                      uint32_t box2 = 1);
 
 // SW-SKA decode: ring-buffer write + split-window attention combined across a cluster
 cudaError_t swska_decode_launch(const void* q, const void* k_new, const void* v_new,

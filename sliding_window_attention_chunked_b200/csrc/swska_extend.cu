@@ -273,7 +273,10 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
     const int sms = device_sm_count();
     if (bf16 && dk == 128 && dv == 128) {
         const int few = max_len < kFewRows ? max_len : kFewRows;
-        route(0, kFewRows, few, kFewTile, (H + kFewHeads - 1) / kFewHeads, sms, 4, 6, N);
+        // Few sequences: four heads a CTA put twice the SMs to work and halve what one SM adds up at the
+        // end; many: eight share a key tile and keep two warps on each scheduler
+        const int heads = (int64_t)N * ((H + kFewHeads - 1) / kFewHeads) >= sms ? kFewHeads : kFewHeads / 2;
+        route(0, kFewRows, few, kFewTile, (H + heads - 1) / heads, sms, 4, 6, N);
         p.short_len = kFewRows;
         if (max_len > kFewRows)
             route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 6, (int64_t)M / kChunkRows + N);

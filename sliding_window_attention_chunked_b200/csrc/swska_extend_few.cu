@@ -10,7 +10,9 @@
 // stages of a key tile and eight value tiles by TMA, 72 KB a stage: three stages hold more than the
 // bytes in flight that HBM's rate times its latency asks of an SM. The pages' rows land in shared
 // memory with the 128-byte swizzle, which keeps the fragment loads free of bank conflicts; a page of
-// any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows.
+// any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows. A warp issues a copy every 100
+// clocks or so, and a tile has to come every 3100 at HBM's rate, so a box takes the rows of all of
+// the CTA's heads: 4 copies a tile for pages of 32 k tokens, 16 for pages of 8 (18 and 72 head by head).
 // Softmax: running maximum and sum in fp32, base 2; the output is rescaled only when a row's maximum
 // moves. Probabilities go to the second product in bf16 (relative 2^-9 each, like the cached values).
 #include <cuda.h>
@@ -66,9 +68,15 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// 16-byte chunk c (of 16) of row r of a tile: two halves of 64 columns, swizzled
+// 16-byte chunk c (of 16) of row r of the key tile: two halves of 64 columns, swizzled
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// Value tiles: [half][box of rows][head][row of the box], so that one box holds every head's rows.
+// Start of the eight rows 8 rg .. 8 rg + 7 of a head in half 0; half 1 is hpg halves further.
+__device__ __forceinline__ uint32_t rows_at(int rg, int head, int hpg, int box) {
+    const int per = box / 8;
+    return (uint32_t)(((rg / per * hpg + head) * per + rg % per) * 1024);
 }
 
 __global__ void __launch_bounds__(NTH, 1)
@@ -104,7 +112,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tc::tma_prefetch_desc(&tm_k);
             tc::tma_prefetch_desc(&tm_v);
         }
-        const int nbox = KT / box, ops = 2 * nbox * (1 + nh);
+        const int nbox = KT / box, ops = 4 * nbox;  // (keys, values) x halves x boxes: at most 16
         int t = 0;  // tiles fed so far
         bool ok = true;
         for (int x = range.lo; x <= range.hi && ok; ++x) {
@@ -126,20 +134,20 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (__shfl_sync(0xffffffffu, pg, b) >= 0) have |= (box == 32 ? 0xffffffffu : ((1u << box) - 1u) << (b * box));
                 if (lane == 0) {
                     mask[s] = have;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(TILE * (1 + nh)));
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
                 }
                 __syncwarp();
-                for (int o0 = 0; o0 < ops; o0 += 32) {
-                    const int op = o0 + lane;
-                    const int b = op % nbox, half = op / nbox % 2, which = op / (2 * nbox);  // 0: keys, 1 + h: values
-                    const int p = __shfl_sync(0xffffffffu, pg, b);
-                    if (op < ops) {
-                        unsigned char* dst = smem + s * stage_bytes + which * TILE + half * HALF + b * box * 128;
-                        const int y = (key0 + b * box) % a.page;
-                        // a page that the table does not have: a coordinate past the end, which fills zeros
-                        if (which == 0) tc::tma_load_3d(dst, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[s]);
-                        else tc::tma_load_3d(dst, &tm_v, half * 64, y, p >= 0 ? p * a.H + h0 + which - 1 : a.P * a.H, &full[s]);
-                    }
+                const int b = lane % nbox, half = lane / nbox % 2;
+                const int p = __shfl_sync(0xffffffffu, pg, b);
+                if (lane < ops) {
+                    unsigned char* dst = smem + s * stage_bytes;
+                    const int y = (key0 + b * box) % a.page;
+                    // a page that the table does not have: a coordinate past the end, which fills zeros
+                    if (lane < 2 * nbox)
+                        tc::tma_load_3d(dst + half * HALF + b * box * 128, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[s]);
+                    else
+                        tc::tma_load_3d(dst + TILE + (half * nbox + b) * hpg * box * 128, &tm_v, half * 64, y,
+                                        p >= 0 ? p * a.H + h0 : a.P * a.H, &full[s]);
                 }
             }
         }
@@ -153,6 +161,8 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int h = h0 + warp;
     const int g = lane / 4, c2 = 2 * (lane % 4);  // this thread's rows g, g + 8 and its column pair
     const int mat = lane / 8, mr = lane % 8;      // this lane's row address in a 4-matrix load
+    // of the values: rows 16 k + 8 (mat & 1) + mr for k = 0, 1
+    const uint32_t vrow[2] = {rows_at(mat & 1, warp, hpg, box) + mr * 128, rows_at(2 + (mat & 1), warp, hpg, box) + mr * 128};
     int t = 0;
     for (int x = range.lo; x <= range.hi; ++x) {
         const ExtendUnit u = load_unit(r.units + x);
@@ -182,7 +192,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = u.kt0; i < u.kt1; ++i, ++t) {
             const int st = t % n_stages, key0 = kt.at(i) * KT;
             if (!wait_warp(&full[st], (uint32_t)((t / n_stages) & 1), abort_flag)) return;
-            const uint32_t kb = smem_u32(smem + st * stage_bytes), vb = kb + (1 + warp) * TILE;
+            const uint32_t kb = smem_u32(smem + st * stage_bytes), vb = kb + TILE;
             float s[4][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -205,14 +215,14 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 // keys that no query sees: the rows behind them may hold anything, so clear this head's
                 const int j = key0 + lane;
                 const bool seen = (have >> lane & 1u) && j <= p1 && ((int64_t)j > (int64_t)p0 - a.W || j < a.S);
-                unsigned drop = ~__ballot_sync(0xffffffffu, seen);
-                zeroed = drop != 0;
-                while (drop) {
-                    const int key = __ffs(drop) - 1;
-                    drop &= drop - 1;
-                    if (lane < 16)
-                        *reinterpret_cast<uint4*>(smem + st * stage_bytes + (1 + warp) * TILE + chunk_at(key, lane)) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                zeroed = !__all_sync(0xffffffffu, seen);
+                if (!seen) {  // lane = key; neighbouring lanes start at neighbouring chunks: no bank conflicts
+                    unsigned char* v = smem + st * stage_bytes + TILE + rows_at(lane / 8, warp, hpg, box) + (lane & 7) * 128;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        *reinterpret_cast<uint4*>(v + ((c + lane) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(v + hpg * HALF + ((c + lane) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
                 __syncwarp();
 #pragma unroll
@@ -272,7 +282,8 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
                     uint32_t b[4];
-                    ldsm4t(vb + chunk_at(16 * k + (mat & 1) * 8 + mr, c + (mat >> 1)), b);
+                    const int ch = c + (mat >> 1);
+                    ldsm4t(vb + vrow[k] + (uint32_t)((ch >> 3) * hpg * HALF + (((ch & 7) ^ mr) << 4)), b);
                     mma16816(o[c], pa, b);
                     mma16816(o[c + 1], pa, b + 2);
                 }
@@ -317,13 +328,18 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) last = atomicAdd(r.count + (int64_t)u.counter * a.H + h, 1) == u.nsplit - 1;
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
         __threadfence();
+        // parts 1, 2, ... lie two part numbers apart
+        const int64_t step = 2 * (int64_t)a.H * r.part_rows;
         for (int row = 0; row < rows; ++row) {
+            const int64_t at0 = r.part_at(u.first, a.H, h, row), at1 = r.part_at(2 * u.c0, a.H, h, row);
+            const float4* x0 = reinterpret_cast<const float4*>(r.part_o + at0 * HD) + lane;
+            const float4* x1 = reinterpret_cast<const float4*>(r.part_o + at1 * HD) + lane;
             // lane = part for the weights (as many as CTAs per head group, at most), lane = four columns for the sum
             float M = -INFINITY, L = 0.f, mv[kMaxParts], w[kMaxParts];
 #pragma unroll
             for (int i = 0; i < kMaxParts; ++i) {
                 const int s = lane + 32 * i;
-                const float2 ml = s < u.nsplit ? __ldcg(&r.part_ml[r.part_at(u.part_of(s), a.H, h, row)]) : make_float2(-INFINITY, 0.f);
+                const float2 ml = s < u.nsplit ? __ldcg(r.part_ml + (s == 0 ? at0 : at1 + s * step)) : make_float2(-INFINITY, 0.f);
                 mv[i] = ml.x;
                 w[i] = ml.y;
                 M = fmaxf(M, ml.x);
@@ -346,9 +362,8 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     float4 x4[16];  // loads in flight together
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        x4[e] = s0 + e < u.nsplit
-                                    ? __ldcg(reinterpret_cast<const float4*>(r.part_o + r.part_at(u.part_of(s0 + e), a.H, h, row) * HD) + lane)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x4[e] = s0 + e < u.nsplit ? __ldcg(s0 + e == 0 ? x0 : x1 + (s0 + e) * (int)step * (HD / 4))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float ws = __shfl_sync(0xffffffffu, mv[i], (s0 + e) & 31);
@@ -374,7 +389,9 @@ cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, c
     CUtensorMap mk, mv;
     cudaError_t e;
     if ((e = make_tmap_bf16_3d(&mk, a.k_pool, HD, (uint64_t)a.page, (uint64_t)a.P, 64, (uint32_t)box)) != cudaSuccess) return e;
-    if ((e = make_tmap_bf16_3d(&mv, a.v_pool, HD, (uint64_t)a.page, (uint64_t)a.P * a.H, 64, (uint32_t)box)) != cudaSuccess) return e;
+    if ((e = make_tmap_bf16_3d_strided(&mv, a.v_pool, HD, (uint64_t)a.page, (uint64_t)a.P * a.H, HD * 2, (uint64_t)a.page * HD * 2,
+                                       64, (uint32_t)box, (uint32_t)hpg)) != cudaSuccess)
+        return e;
     int stages = RING / (TILE * (1 + hpg));
     if (stages > MAXST) stages = MAXST;
     if ((e = cudaFuncSetAttribute(extend_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;

@@ -341,8 +341,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         unsigned char* vr = smem + OFF_RING + (Lv % NSLOT) * TILE_BYTES + row * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4*>(vr + HALF_BYTES + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                            // neighbouring threads start at neighbouring chunks: no bank conflicts
+                            const int o16 = 16 * ((c + row) & 7);
+                            *reinterpret_cast<uint4*>(vr + o16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(vr + HALF_BYTES + o16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                         tc::fence_proxy_async();
                     }

@@ -43,12 +43,13 @@ cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, bool fp32, uint64_t
 }
 
 cudaError_t make_tmap_bf16_3d_strided(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                                      uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1) {
+                                      uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1,
+                                      uint32_t box2) {
     auto fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {d0, d1, d2};
     const cuuint64_t strides[2] = {stride1, stride2};
-    const cuuint32_t box[3] = {box0, box1, 1};
+    const cuuint32_t box[3] = {box0, box1, box2};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
