@@ -79,6 +79,10 @@ __device__ __forceinline__ uint32_t rows_at(int rg, int head, int hpg, int box) 
     return (uint32_t)(((rg / per * hpg + head) * per + rg % per) * 1024);
 }
 
+// bits 0 .. x and bits x .. 31 of a word, for any x
+__device__ __forceinline__ uint32_t bits_to(int x) { return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u); }
+__device__ __forceinline__ uint32_t bits_from(int64_t x) { return x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x); }
+
 __global__ void __launch_bounds__(NTH, 1)
 extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const ExtendArgs a, const ExtendRoute r, int hpg, int n_stages, int box, float scale_log2) {
@@ -225,14 +229,21 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                 }
                 __syncwarp();
+                // bit per key: seen by row g (v[0]) and by row g + 8 (v[1])
+                uint32_t v[2];
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int e = 0; e < 2; ++e) {
+                    const int p = p0 + g + 8 * e;
+                    v[e] = have & bits_to(p - key0) & (bits_from((int64_t)p - a.W + 1 - key0) | bits_to(a.S - 1 - key0));
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = 8 * n + c2 + (e & 1), key = key0 + c, p = p0 + g + (e & 2) * 4;
-                        const bool see = (have >> c & 1u) && key <= p && ((int64_t)key > (int64_t)p - a.W || key < a.S);
-                        if (!see) s[n][e] = -INFINITY;
-                    }
+                for (int n = 0; n < 4; ++n) {
+                    const int c = 8 * n + c2;
+                    if (!(v[0] >> c & 1u)) s[n][0] = -INFINITY;
+                    if (!(v[0] >> c & 2u)) s[n][1] = -INFINITY;
+                    if (!(v[1] >> c & 1u)) s[n][2] = -INFINITY;
+                    if (!(v[1] >> c & 2u)) s[n][3] = -INFINITY;
+                }
             }
             // row maxima over the four threads of a row
             float mx[2] = {-INFINITY, -INFINITY};
@@ -330,7 +341,47 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __threadfence();
         // parts 1, 2, ... lie two part numbers apart
         const int64_t step = 2 * (int64_t)a.H * r.part_rows;
-        for (int row = 0; row < rows; ++row) {
+        if (rows > 1) {
+            // several rows, few parts: lane = row for the weights, eight rows' loads in flight
+            const int64_t at0 = r.part_at(u.first, a.H, h, 0), at1 = r.part_at(2 * u.c0, a.H, h, 0);
+            auto part0 = [&](int s) { return s == 0 ? at0 : at1 + s * step; };  // the part's row 0
+            const bool in = lane < rows;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+            for (int s = 0; s < u.nsplit; ++s) {
+                const float2 ml = in ? __ldcg(r.part_ml + part0(s) + lane) : make_float2(-INFINITY, 0.f);
+                const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
+                L = fmaf(ml.y, tc::ex2(ml.x - base), L * tc::ex2(M - base));
+                M = mn;
+            }
+            const float base = M == -INFINITY ? 0.f : M, inv = L == 0.f ? 0.f : 1.f / L;
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+                float4 O[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int s = 0; s < u.nsplit; ++s) {
+                    const int64_t at = part0(s);
+                    const float w = in ? tc::ex2(__ldcg(&r.part_ml[at + lane].x) - base) * inv : 0.f;
+                    const float4* x = reinterpret_cast<const float4*>(r.part_o + (at + r0) * HD) + lane;
+                    float4 x4[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x4[i] = r0 + i < rows ? __ldcg(x + i * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float wi = __shfl_sync(0xffffffffu, w, r0 + i);
+                        O[i].x = fmaf(x4[i].x, wi, O[i].x);
+                        O[i].y = fmaf(x4[i].y, wi, O[i].y);
+                        O[i].z = fmaf(x4[i].z, wi, O[i].z);
+                        O[i].w = fmaf(x4[i].w, wi, O[i].w);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (r0 + i < rows) store4(out + ((row0 + r0 + i) * a.H + h) * HD + 4 * lane, O[i]);
+            }
+        } else {
+            const int row = 0;
             const int64_t at0 = r.part_at(u.first, a.H, h, row), at1 = r.part_at(2 * u.c0, a.H, h, row);
             const float4* x0 = reinterpret_cast<const float4*>(r.part_o + at0 * HD) + lane;
             const float4* x1 = reinterpret_cast<const float4*>(r.part_o + at1 * HD) + lane;

@@ -85,6 +85,10 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     return d;
 }
 
+// bits 0 .. x and bits x .. 31 of a word, for any x
+__device__ __forceinline__ uint32_t bits_to(int x) { return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u); }
+__device__ __forceinline__ uint32_t bits_from(int64_t x) { return x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x); }
+
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const ExtendArgs a, const ExtendRoute r, int box,
@@ -329,11 +333,17 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool all_there = there == 0xffffu;
                 const bool in_reach = key0 > p1 - a.W || key0 + (BN - 1) < a.S;  // every key, for every row
                 if (!all_there || !in_reach || key0 + (BN - 1) > p0) {
-                    const int64_t lo64 = (int64_t)p - key0 - a.W + 1;
-                    const int lo = lo64 > 0 ? (int)lo64 : 0, hi = p - key0, first = a.S - key0;
+                    // bit per key: 32 keys a word, four page bits of eight keys each
+                    const int64_t lo = (int64_t)p - key0 - a.W + 1;
+                    const int hi = p - key0, first = a.S - 1 - key0;
 #pragma unroll
-                    for (int c = 0; c < BN; ++c)
-                        if ((c < lo && c >= first) || c > hi || !(there >> (c / 8) & 1u)) s[c] = 0xff800000u;
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t pages = (((there >> (4 * w) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
+                        const uint32_t v = pages & bits_to(hi - 32 * w) & (bits_from(lo - 32 * w) | bits_to(first - 32 * w));
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(v >> c & 1u)) s[32 * w + c] = 0xff800000u;
+                    }
                     // this thread's value row, if no query of the tile sees it
                     const int key = key0 + row;
                     const bool seen = (there >> (row / 8) & 1u) && key <= p1 && (key > p0 - a.W || key < a.S);
