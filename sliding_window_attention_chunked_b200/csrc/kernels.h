@@ -159,8 +159,6 @@ struct SinkArgs {
     float scale;
     void* workspace;
 };
-cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
-cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
 cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t s);  // bf16, dk = dv = 128, T >= 128
 cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s);
 cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s);

@@ -43,20 +43,23 @@ int64_t tpad(int T) { return ((int64_t)T + 127) / 128 * 128; }
 
 }  // namespace
 
-SinkParts sink_parts_plan(const SinkArgs& a, int size, int G) {
+SinkParts sink_parts_plan(const SinkArgs& a, int ks, int qs, int G) {
     SinkParts p;
+    p.ks = ks;
+    p.qs = qs;
+    p.nk = (a.T + ks - 1) / ks;
+    p.nq = (a.T + qs - 1) / qs;
     p.G = G;
     p.B = a.B;
     p.H = a.H;
     p.T = a.T;
+    p.W = a.W;
     p.dk = a.d_k;
     p.dv = a.d_v;
     p.R = a.S < a.T ? a.S : a.T;
-    const int tiles = (a.T + size - 1) / size;
-    const int far = tiles - 1 - SinkParts::near_hi(0, tiles, size, a.W);  // the first tile has the most
+    const int near = SinkParts::near_hi(0, ks, qs, p.nq, a.W) + 1, far = p.nq - near;  // the first tile has the most
     if (p.R > 0 && far > 0) {
-        const int near = SinkParts::near_hi(0, tiles, size, a.W) + 1;
-        p.n_tiles = (p.R + size - 1) / size;
+        p.n_tiles = (p.R + ks - 1) / ks;
         // a segment is a window long, at least 4 tiles (its sums are S rows of memory traffic), and
         // there are at most 64 of them
         p.seg_len = near > 4 ? near : 4;

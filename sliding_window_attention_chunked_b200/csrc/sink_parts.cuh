@@ -18,29 +18,32 @@ struct SinkWork {
 };
 
 struct SinkParts {
-    int n_tiles = 0, nseg = 0, seg_len = 0;  // tiles with far queries, segments each, query tiles per segment
-    int G = 0, B = 0, H = 0, T = 0, R = 0, dk = 0, dv = 0;  // head groups of dk; R = min(S, T) rows
+    int ks = 0, qs = 0, nk = 0, nq = 0;        // rows of a key tile and of a query tile, and their numbers
+    int n_tiles = 0, nseg = 0, seg_len = 0;    // key tiles with far queries, segments each, query tiles per segment
+    int G = 0, B = 0, H = 0, T = 0, W = 0, R = 0, dk = 0, dv = 0;  // head groups of dk; R = min(S, T) rows
     float* dk_part = nullptr;  // [G][B][T][dk]       near sums of every key
     float* dv_far = nullptr;   // [1 + nseg][B H][R][dv]
     float* dk_far = nullptr;   // [nseg][G][B][R][dk]
 
-    __host__ __device__ static int near_hi(int tile, int tiles, int size, int W) {
-        const int64_t last = ((int64_t)tile * size + size - 1 + W - 1) / size;
-        return last < tiles - 1 ? (int)last : tiles - 1;
+    // the last query tile that sees a key tile through the window
+    __host__ __device__ static int near_hi(int tile, int ks, int qs, int nq, int W) {
+        const int64_t last = ((int64_t)tile * ks + ks - 1 + W - 1) / qs;
+        return last < nq - 1 ? (int)last : nq - 1;
     }
-    __device__ __forceinline__ SinkWork work(int x, int tiles, int size, int T_, int W) const {
+    __host__ __device__ int ctas() const { return nk + n_tiles * nseg; }
+    __device__ __forceinline__ SinkWork work(int x) const {
         SinkWork w;
-        if (x < tiles) {
+        if (x < nk) {
             w.tile = x;
             w.slot = 0;
-            w.q_lo = x;
-            w.q_hi = near_hi(x, tiles, size, W);
+            w.q_lo = x * ks / qs;
+            w.q_hi = near_hi(x, ks, qs, nq, W);
         } else {
-            w.tile = (x - tiles) / nseg;
-            const int g = (x - tiles) % nseg;
+            w.tile = (x - nk) / nseg;
+            const int g = (x - nk) % nseg;
             w.slot = 1 + g;
-            w.q_lo = near_hi(w.tile, tiles, size, W) + 1 + g * seg_len;
-            w.q_hi = w.q_lo + seg_len - 1 < tiles - 1 ? w.q_lo + seg_len - 1 : tiles - 1;
+            w.q_lo = near_hi(w.tile, ks, qs, nq, W) + 1 + g * seg_len;
+            w.q_hi = w.q_lo + seg_len - 1 < nq - 1 ? w.q_lo + seg_len - 1 : nq - 1;
         }
         return w;
     }
@@ -52,8 +55,8 @@ struct SinkParts {
     }
 };
 
-// the split for tiles of `size` rows and G head groups (pointers not set)
-SinkParts sink_parts_plan(const SinkArgs& a, int size, int G);
+// the split for key tiles of ks rows, query tiles of qs and G head groups (pointers not set)
+SinkParts sink_parts_plan(const SinkArgs& a, int ks, int qs, int G);
 // floats of workspace: row statistics (two arrays of T rounded up to 128 rows), then the parts
 size_t sink_parts_floats(const SinkParts& p);
 // sets the pointers inside a.workspace; returns the statistics array (2 B H Tpad floats)

@@ -510,11 +510,11 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int grp = blockIdx.y, b = blockIdx.z;
     int kt = blockIdx.x, qt_lo = kt;  // queries t in [j, j + W - 1] see key j
-    int qt_hi = SinkParts::near_hi(kt, n_qtiles, TILE, W);  // the last query tile that sees the tile
+    int qt_hi = SinkParts::near_hi(kt, TILE, TILE, n_qtiles, W);  // the last query tile that sees the tile
     int slot = 0;
     const int S = SINK ? S_arg : 0;
     if (SINK) {
-        const SinkWork wk = parts.work((int)blockIdx.x, n_qtiles, TILE, T, W);
+        const SinkWork wk = parts.work((int)blockIdx.x);
         kt = wk.tile;
         qt_lo = wk.q_lo;
         qt_hi = wk.q_hi;
@@ -959,7 +959,7 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     const int64_t Tpad = swska_backward_tc_tpad(T);
     if (B > 65535) return cudaErrorInvalidConfiguration;
     const int G = swska_backward_tc_groups(B, H, T);
-    SinkParts parts = sink_parts_plan(a, TILE, G);
+    SinkParts parts = sink_parts_plan(a, TILE, TILE, G);
     float* nlse2 = sink_parts_bind(parts, a);
     float* dbuf = nlse2 + (size_t)B * H * Tpad;
     // launch 1: the row statistics from the forward's output and log-sum-exp
@@ -984,7 +984,7 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     const float sl = a.scale * kLog2e;
     ska_bwd_dq_kernel<true><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM_SINK, stream>>>(
         mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S);
-    ska_bwd_dkdv_kernel<true><<<dim3((unsigned)(nqt + parts.n_tiles * parts.nseg), (unsigned)G, (unsigned)B),
+    ska_bwd_dkdv_kernel<true><<<dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B),
                                 NTHREADS_KEY, ka::SMEM, stream>>>(
         mq, mdo, mk, mv, nlse2, dbuf, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T, (int)Tpad, H, H / G, W,
         sl, nqt, a.S, parts);

@@ -108,6 +108,8 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
     __syncthreads();
     wait_for_launch_before();
+    // the chunks' kernel (swska_extend_tc.cu) may take over SMs as they fall free
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const ExtendRange range = load_range(r, blockIdx.x / r.groups);
 
     if (warp == kFewHeads) {

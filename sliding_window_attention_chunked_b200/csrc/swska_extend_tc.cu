@@ -138,7 +138,9 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_holder;
-    wait_for_launch_before();
+    // This launch comes after the one for few tokens (swska_extend_few.cu), which lets it start once
+    // all of its CTAs have seen the end of the launch that wrote the units and the cache: the two share
+    // the GPU, and only the end of this one waits for the other.
     // neighbouring CTAs take the head pairs of one chunk: they share its keys in L2
     const int hp = blockIdx.x % r.groups;
     const int head[2] = {2 * hp, min(2 * hp + 1, a.H - 1)};  // an odd H's last pair has one head twice
@@ -515,6 +517,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 9) tc::tmem_dealloc(tmem, 512);
+    wait_for_launch_before();
 }
 
 }  // namespace

@@ -1,12 +1,14 @@
-// swska_sink_simt.cu -- SW-SKA with first tokens that stay visible, forward and backward on CUDA
+// swska_sink_simt.cuh -- SW-SKA with first tokens that stay visible, forward and backward on CUDA
 // cores (every product an fp32 FMA): fp32 inputs, and bf16 shapes outside the tensor-core kernels.
 //
 // Query t sees the keys j <= t with j > t - W or j < S:
 //   p_tj = softmax_j(scale q_t . k_j),  o_t = sum_j p_tj v_j,  lse_t = log sum_j exp(scale q_t . k_j)
 //   D_t = dO_t . o_t,  dS_tj = p_tj (dO_t . v_j - D_t)
 //   dq_t = scale sum_j dS_tj k_j,  dv_j = sum_t p_tj dO_t,  dk_j = scale sum_h sum_t dS_tj q_t
-// One CTA per 64 queries of a head (forward, dq) or per 64 keys of a head (dk, dv), with the
-// tiles of simt_tile.cuh; it visits the tiles that its rows can see and masks inside them. The
+// One CTA per BQ queries of a head (forward, dq) or per BQ keys of a head (dk, dv), with the
+// tiles of simt_tile.cuh; it visits the tiles that its rows can see and masks inside them. BQ is 64,
+// or 32 or 16 where that many rows would leave SMs without work (T 1000, 4 heads, fp32, d_k 64, d_v 128,
+// window 256: 64 CTAs of 64 rows take 215 us a step). The
 // kernels are bound by FMA issue: a 64 x 64 tile of head dim 128 is 1 M FMAs per product against 64 KB
 // of tile loads that stay in L2.
 //
@@ -14,6 +16,8 @@
 // tile. Its queries past the window are dealt out in segments to further CTAs, each with its own
 // partial sums for the S rows; the last launch adds the parts in a fixed order, so the result does
 // not depend on timing. The same launch adds the heads' parts of the shared dk.
+#pragma once
+
 #include <math.h>
 
 #include "kernels.h"
@@ -25,12 +29,10 @@ namespace {
 
 using namespace simt;
 
-constexpr int BQ = 64;
-constexpr int NTH = 4 * BQ;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int DK, int DV>
+template <int DK, int DV, int BQ>
 constexpr int fwd_smem() { return (BQ * ld<DK>() + BK * ld<DK>() + BK * ld<DV>() + BQ * LDP) * 4; }
 
 // key tiles of a query tile: those of the first S keys that lie before the window's, then the window's
@@ -47,11 +49,12 @@ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int W, int S) {
     return k;
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(NTH)
+template <int DK, int DV, int BQ>
+__global__ void __launch_bounds__(4 * BQ)
 sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                 void* __restrict__ o, float* __restrict__ lse, bool bf16, int H, int T, int W, int S, float scale_log2,
                 int qtiles) {
+    constexpr int NTH = 4 * BQ;
     extern __shared__ __align__(16) float sm[];
     float* sQ = sm;
     float* sK = sQ + BQ * ld<DK>();
@@ -101,19 +104,20 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int BQ>
 constexpr int dq_smem() { return (BQ * (ld<DK>() + ld<DV>()) + BK * (ld<DK>() + ld<DV>()) + BQ * LDP) * 4; }
 
 // With bf16 rows D from the stored o is off by about 2^-9 of it, which a row whose attention is peaked
 // turns into a larger error of dS = p (dP - D): there D0 from o only centres the sums, and
 //   e = sum_j p_j (dP_j - D0),  dq = scale (sum_j p_j (dP_j - D0) k_j - e sum_j p_j k_j),  D = D0 + e
 // gives the row's own D in the same pass, for one more product per tile.
-template <int DK, int DV, bool BF16>
-__global__ void __launch_bounds__(NTH)
+template <int DK, int DV, int BQ, bool BF16>
+__global__ void __launch_bounds__(4 * BQ)
 sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                const void* __restrict__ o, const float* __restrict__ lse, const void* __restrict__ dO,
                void* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     constexpr bool bf16 = BF16;
+    constexpr int NTH = 4 * BQ;
     extern __shared__ __align__(16) float sm[];
     float* sQ = sm;
     float* sG = sQ + BQ * ld<DK>();
@@ -194,33 +198,33 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
     }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int BQ>
 constexpr int dkv_smem() {
-    return (2 * BK * (ld<DK>() + ld<DV>()) + BK * LDP + 2 * BK) * 4;
+    return ((BQ + BK) * (ld<DK>() + ld<DV>()) + BQ * LDP + 2 * BK) * 4;
 }
 
 // blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
-template <int DK, int DV>
-__global__ void __launch_bounds__(NTH)
+template <int DK, int DV, int BQ>
+__global__ void __launch_bounds__(4 * BQ)
 sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                 const float* __restrict__ lse, const float* __restrict__ dbuf, const void* __restrict__ dO,
-                void* __restrict__ dv, SinkParts parts, bool bf16, int B, int H, int T, int W, int S, float scale,
-                int tiles) {
+                void* __restrict__ dv, SinkParts parts, bool bf16, int B, int H, int T, int W, int S, float scale) {
+    constexpr int NTH = 4 * BQ;
     extern __shared__ __align__(16) float sm[];
     float* sK = sm;
-    float* sV = sK + BK * ld<DK>();
-    float* sQ = sV + BK * ld<DV>();
+    float* sV = sK + BQ * ld<DK>();
+    float* sQ = sV + BQ * ld<DV>();
     float* sG = sQ + BK * ld<DK>();
     float* sP = sG + BK * ld<DV>();
-    float* sL = sP + BK * LDP;
+    float* sL = sP + BQ * LDP;
     float* sD = sL + BK;
     const int h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = (int64_t)b * H + h;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const SinkWork w = parts.work((int)blockIdx.x, tiles, BK, T, W);
-    const int key0 = w.tile * BK;
-    load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
-    load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    const SinkWork w = parts.work((int)blockIdx.x);
+    const int key0 = w.tile * BQ;
+    load_tile<DK, BQ, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
+    load_tile<DV, BQ, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
     const float scale_log2 = scale * kLog2e;
     float ak[4][DK / 16], av[4][DV / 16];
 #pragma unroll
@@ -280,88 +284,77 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int BQ>
 cudaError_t fwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
+    constexpr int smem = fwd_smem<DK, DV, BQ>();
     const int qtiles = (a.T + BQ - 1) / BQ;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         fwd_smem<DK, DV>());
+    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    sink_fwd_kernel<DK, DV><<<(unsigned)grid, NTH, fwd_smem<DK, DV>(), s>>>(
+    sink_fwd_kernel<DK, DV, BQ><<<(unsigned)grid, 4 * BQ, smem, s>>>(
         a.q, a.k, a.v, a.out, a.lse_out, bf16, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
     note_launches(1);
     return cudaGetLastError();
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int BQ>
 cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
-    const int tiles = (a.T + BQ - 1) / BQ;
-    const int64_t grid = (int64_t)tiles * a.B * a.H;
+    constexpr int q_smem = dq_smem<DK, DV, BQ>(), kv_smem = dkv_smem<DK, DV, BQ>();
+    const int qtiles = (a.T + BQ - 1) / BQ;
+    const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL || a.B > 65535) return cudaErrorInvalidConfiguration;
-    SinkParts parts = sink_parts_plan(a, BK, a.H);
+    SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, true> : sink_dq_kernel<DK, DV, false>;
-    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  dq_smem<DK, DV>())) != cudaSuccess)
+    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, BQ, true> : sink_dq_kernel<DK, DV, BQ, false>;
+    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem)) != cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  dkv_smem<DK, DV>())) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem)) !=
+        cudaSuccess)
         return e;
-    dq_kernel<<<(unsigned)grid, NTH, dq_smem<DK, DV>(), s>>>(
-        a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W, a.S, a.scale, tiles);
-    sink_dkv_kernel<DK, DV><<<dim3((unsigned)(tiles + parts.n_tiles * parts.nseg), (unsigned)a.H, (unsigned)a.B), NTH,
-                              dkv_smem<DK, DV>(), s>>>(a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H,
-                                                       a.T, a.W, a.S, a.scale, tiles);
+    dq_kernel<<<(unsigned)grid, 4 * BQ, q_smem, s>>>(a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W, a.S,
+                                                     a.scale, qtiles);
+    sink_dkv_kernel<DK, DV, BQ><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), 4 * BQ, kv_smem, s>>>(
+        a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H, a.T, a.W, a.S, a.scale);
     note_launches(2);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, bf16, s);
 }
 
+// rows per CTA: the most that still gives every SM work
+int rows_for(int B, int H, int T) {
+    const int64_t want = device_sm_count();
+    for (int rows = 64; rows > 16; rows /= 2)
+        if ((int64_t)B * H * ((T + rows - 1) / rows) >= want) return rows;
+    return 16;
+}
+
+template <int DK, int DV>
+cudaError_t pick_rows(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    switch (rows_for(a.B, a.H, a.T)) {
+        case 64: return backward ? bwd_t<DK, DV, 64>(a, bf16, s) : fwd_t<DK, DV, 64>(a, bf16, s);
+        case 32: return backward ? bwd_t<DK, DV, 32>(a, bf16, s) : fwd_t<DK, DV, 32>(a, bf16, s);
+        default: return backward ? bwd_t<DK, DV, 16>(a, bf16, s) : fwd_t<DK, DV, 16>(a, bf16, s);
+    }
+}
+
 template <int DK>
 cudaError_t pick_dv(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
     switch (a.d_v) {
-        case 16: return backward ? bwd_t<DK, 16>(a, bf16, s) : fwd_t<DK, 16>(a, bf16, s);
-        case 32: return backward ? bwd_t<DK, 32>(a, bf16, s) : fwd_t<DK, 32>(a, bf16, s);
-        case 64: return backward ? bwd_t<DK, 64>(a, bf16, s) : fwd_t<DK, 64>(a, bf16, s);
-        case 128: return backward ? bwd_t<DK, 128>(a, bf16, s) : fwd_t<DK, 128>(a, bf16, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
-cudaError_t pick(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
-    switch (a.d_k) {
-        case 16: return pick_dv<16>(a, bf16, backward, s);
-        case 32: return pick_dv<32>(a, bf16, backward, s);
-        case 64: return pick_dv<64>(a, bf16, backward, s);
-        case 128: return pick_dv<128>(a, bf16, backward, s);
+        case 16: return pick_rows<DK, 16>(a, bf16, backward, s);
+        case 32: return pick_rows<DK, 32>(a, bf16, backward, s);
+        case 64: return pick_rows<DK, 64>(a, bf16, backward, s);
+        case 128: return pick_rows<DK, 128>(a, bf16, backward, s);
     }
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t swska_sink_prefill_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, false, s); }
-cudaError_t swska_sink_backward_simt_launch(const SinkArgs& a, bool bf16, cudaStream_t s) { return pick(a, bf16, true, s); }
-
-// bf16 with 128-wide heads and at least one full tile runs on the tensor cores
-cudaError_t swska_sink_prefill_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
-    if (bf16 && swska_prefill_tc_supported(a.H, a.T, a.d_k, a.d_v))
-        return swska_prefill_tc_stats_launch(a.q, a.k, a.v, a.out, nullptr, a.lse_out, nullptr, a.T, a.B, a.H, a.T, a.W,
-                                             a.scale, s, kLn2, a.S);
-    return swska_sink_prefill_simt_launch(a, bf16, s);
-}
-cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_t s) {
-    if (bf16 && swska_backward_tc_supported(a.H, a.T, a.d_k, a.d_v)) return swska_sink_backward_tc_launch(a, s);
-    return swska_sink_backward_simt_launch(a, bf16, s);
-}
-size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S) {
-    SinkArgs a{};
-    a.B = B, a.H = H, a.T = T, a.d_k = dk, a.d_v = dv, a.W = W, a.S = S;
-    // enough for either route: tiles of 64 or 128 keys, at most H head groups
-    const size_t x = sink_parts_floats(sink_parts_plan(a, BK, H)), y = sink_parts_floats(sink_parts_plan(a, 128, H));
-    return (x > y ? x : y) * sizeof(float);
-}
+// forward or backward for one key head dim (an instance each in swska_sink_simt_<dk>.cu, which
+// compile side by side)
+template <int DK>
+cudaError_t sink_simt_launch(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s);
 
 }  // namespace rod

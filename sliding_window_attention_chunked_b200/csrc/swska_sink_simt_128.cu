@@ -1,0 +1,11 @@
+// swska_sink_simt_128.cu -- the kernels of swska_sink_simt.cuh for key head dim 128.
+#include "swska_sink_simt.cuh"
+
+namespace rod {
+
+template <>
+cudaError_t sink_simt_launch<128>(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    return pick_dv<128>(a, bf16, backward, s);
+}
+
+}  // namespace rod

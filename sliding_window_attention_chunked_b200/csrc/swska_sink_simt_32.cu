@@ -1,0 +1,11 @@
+// swska_sink_simt_32.cu -- the kernels of swska_sink_simt.cuh for key head dim 32.
+#include "swska_sink_simt.cuh"
+
+namespace rod {
+
+template <>
+cudaError_t sink_simt_launch<32>(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    return pick_dv<32>(a, bf16, backward, s);
+}
+
+}  // namespace rod

@@ -1,0 +1,11 @@
+// swska_sink_simt_64.cu -- the kernels of swska_sink_simt.cuh for key head dim 64.
+#include "swska_sink_simt.cuh"
+
+namespace rod {
+
+template <>
+cudaError_t sink_simt_launch<64>(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+    return pick_dv<64>(a, bf16, backward, s);
+}
+
+}  // namespace rod
