@@ -6,10 +6,13 @@
 // 4 ty + i and columns tx + 16 j, and of a BQ x D product rows 4 ty + i and D / 16 columns. Tiles
 // sit in shared memory as fp32 rows of D + 4 floats: the pad moves neighbouring rows by four
 // banks, so that the 16-byte loads of eight neighbouring rows touch every bank once. A 4-wide step
-// of a score product is then 8 16-byte loads for 64 FMAs.
+// of a score product is then 8 16-byte loads for 64 FMAs, which go out two to an instruction
+// (fma.rn.f32x2): along d in a score product (even and odd terms summed apart), along the columns in
+// a product of probabilities. That leaves the issue slots that the loads need.
 #pragma once
 
 #include "common.cuh"
+#include "exp2x2.cuh"
 
 namespace rod {
 namespace simt {
@@ -34,8 +37,8 @@ __device__ __forceinline__ void store1_as(void* p, bool bf16, int64_t i, float f
 // ROWS rows of D elements into fp32 rows of D + 4; at(r) gives the element offset of row r, or -1
 // for a row of zeros
 template <int D, int ROWS, int NTH, typename At>
-__device__ __forceinline__ void load_tile(float* s, const void* base, bool bf16, At at) {
-    for (int i = threadIdx.x; i < ROWS * (D / 4); i += NTH) {
+__device__ __forceinline__ void load_tile(float* s, const void* base, bool bf16, At at, int tid = threadIdx.x) {
+    for (int i = tid; i < ROWS * (D / 4); i += NTH) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
         const int64_t off = at(r);
         const float4 x = off >= 0 ? load4_as(base, bf16, off + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -46,10 +49,11 @@ __device__ __forceinline__ void load_tile(float* s, const void* base, bool bf16,
 // acc[i][j] = a_row(4 ty + i) . b_row(tx + 16 j)
 template <int D>
 __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty, int tx, float acc[4][4]) {
+    float2 sum[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sum[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
         float4 x[4], y[4];
@@ -61,12 +65,14 @@ __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty,
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+                sum[i][j] = fx::f2fma(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]);
+                sum[i][j] = fx::f2fma(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), sum[i][j]);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = sum[i][j].x + sum[i][j].y;
 }
 
 // columns of a BQ x D accumulator held by thread column tx: groups of VW neighbours
@@ -107,11 +113,26 @@ __device__ __forceinline__ void tile_mul(const float* w, const float* x, int ty,
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (C::N == 1) {
+                    acc[i][0] = fmaf(p[i][u], v[0], acc[i][0]);
+                } else {
 #pragma unroll
-                for (int c = 0; c < C::N; ++c) acc[i][c] = fmaf(p[i][u], v[c], acc[i][c]);
+                    for (int c = 0; c < C::N; c += 2) {
+                        const float2 t = fx::f2fma(make_float2(p[i][u], p[i][u]), make_float2(v[c], v[c + 1]),
+                                                   make_float2(acc[i][c], acc[i][c + 1]));
+                        acc[i][c] = t.x;
+                        acc[i][c + 1] = t.y;
+                    }
+                }
+            }
         }
     }
+}
+
+// the NTH threads of group g of a CTA meet (barrier 0 is the CTA's)
+template <int NTH> __device__ __forceinline__ void group_sync(int g) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(NTH) : "memory");
 }
 
 // sum / maximum over the 16 threads of a row group (lanes that differ in tx)

@@ -38,13 +38,9 @@ cudaError_t swska_sink_backward_launch(const SinkArgs& a, bool bf16, cudaStream_
 size_t swska_sink_backward_workspace_size(int B, int H, int T, int dk, int dv, int W, int S) {
     SinkArgs a{};
     a.B = B, a.H = H, a.T = T, a.d_k = dk, a.d_v = dv, a.W = W, a.S = S;
-    // enough for either route and any tile of keys, with at most H head groups
-    size_t most = sink_parts_floats(sink_parts_plan(a, 128, 128, H));
-    for (int ks = 16; ks <= 64; ks *= 2) {
-        const size_t x = sink_parts_floats(sink_parts_plan(a, ks, 64, H));
-        most = x > most ? x : most;
-    }
-    return most * sizeof(float);
+    // enough for either route (their key and query tiles), with at most H head groups
+    const size_t x = sink_parts_floats(sink_parts_plan(a, 32, 64, H)), y = sink_parts_floats(sink_parts_plan(a, 128, 128, H));
+    return (x > y ? x : y) * sizeof(float);
 }
 
 }  // namespace rod

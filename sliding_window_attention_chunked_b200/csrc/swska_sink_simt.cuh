@@ -5,10 +5,12 @@
 //   p_tj = softmax_j(scale q_t . k_j),  o_t = sum_j p_tj v_j,  lse_t = log sum_j exp(scale q_t . k_j)
 //   D_t = dO_t . o_t,  dS_tj = p_tj (dO_t . v_j - D_t)
 //   dq_t = scale sum_j dS_tj k_j,  dv_j = sum_t p_tj dO_t,  dk_j = scale sum_h sum_t dS_tj q_t
-// One CTA per BQ queries of a head (forward, dq) or per BQ keys of a head (dk, dv), with the
-// tiles of simt_tile.cuh; it visits the tiles that its rows can see and masks inside them. BQ is 64,
-// or 32 or 16 where that many rows would leave SMs without work (T 1000, 4 heads, fp32, d_k 64, d_v 128,
-// window 256: 64 CTAs of 64 rows take 215 us a step). The
+// One CTA per 32 queries of a head (forward, dq) or per 32 keys of a head (dk, dv), with the tiles of
+// simt_tile.cuh; it visits the tiles that its rows can see and masks inside them. What a tile costs is
+// mostly waiting (loads, then products of a few warps), so up to four groups of 128 threads share a
+// CTA's tiles in turn, each with its own buffers and sums, which are added at the end in the order of
+// the groups (fp32, T 1000, 4 heads, d_k 64, d_v 128, window 256: one group of 256 threads and 64 rows a
+// CTA takes 215 us a step). The
 // kernels are bound by FMA issue: a 64 x 64 tile of head dim 128 is 1 M FMAs per product against 64 KB
 // of tile loads that stay in L2.
 //
@@ -32,8 +34,44 @@ using namespace simt;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int DK, int DV, int BQ>
-constexpr int fwd_smem() { return (BQ * ld<DK>() + BK * ld<DK>() + BK * ld<DV>() + BQ * LDP) * 4; }
+constexpr int BQ = 32;
+constexpr int NTH = 4 * BQ;  // threads of a group
+// groups that fit: `own` floats for all, `each` per group, 227 KB in all
+constexpr int groups_for(int own, int each) {
+    const int n = (56 * 1024 - own) / each;
+    return n < 4 ? n : 4;
+}
+// forward: Q | per group K, V, P
+template <int DK, int DV> struct Fwd {
+    static constexpr int own = BQ * ld<DK>(), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP;
+    static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
+};
+// dq: Q, dO | per group K, V, dS
+template <int DK, int DV> struct Dq {
+    static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP;
+    static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
+};
+// dk, dv: K, V | per group Q, dO, P, log-sum-exp, D
+template <int DK, int DV> struct Dkv {
+    static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP + 2 * BK;
+    static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
+};
+
+// a group's sums (rows 4 ty + i, N columns a thread) to and from its buffers
+template <int N>
+__device__ __forceinline__ void put_sums(float* w, int tid, const float acc[4][N]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) w[(i * N + c) * NTH + tid] = acc[i][c];
+}
+template <int N>
+__device__ __forceinline__ void add_sums(const float* w, int tid, float acc[4][N]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[i][c] += w[(i * N + c) * NTH + tid];
+}
 
 // key tiles of a query tile: those of the first S keys that lie before the window's, then the window's
 struct KeyTiles {
@@ -49,37 +87,40 @@ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int W, int S) {
     return k;
 }
 
-template <int DK, int DV, int BQ>
-__global__ void __launch_bounds__(4 * BQ)
+template <int DK, int DV>
+__global__ void __launch_bounds__(NTH * Fwd<DK, DV>::NG)
 sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                 void* __restrict__ o, float* __restrict__ lse, bool bf16, int H, int T, int W, int S, float scale_log2,
                 int qtiles) {
-    constexpr int NTH = 4 * BQ;
+    constexpr int NG = Fwd<DK, DV>::NG, N = DV / 16;
     extern __shared__ __align__(16) float sm[];
+    const int g = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sQ = sm;
-    float* sK = sQ + BQ * ld<DK>();
+    float* mine = sm + Fwd<DK, DV>::own + g * Fwd<DK, DV>::each;
+    float* sK = mine;
     float* sV = sK + BK * ld<DK>();
     float* sP = sV + BK * ld<DV>();
     const int64_t bh = blockIdx.x / qtiles, b = bh / H;
     const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
-    load_tile<DK, BQ, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    load_tile<DK, BQ, NTH * NG>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    __syncthreads();
     const KeyTiles kt = key_tiles(t0, t1, W, S);
-    float m[4], l[4], acc[4][DV / 16];
+    float m[4], l[4], acc[4][N];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < DV / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < N; ++c) acc[i][c] = 0.f;
     }
-    for (int it = 0; it < kt.n; ++it) {
+    for (int it = g; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
-        __syncthreads();
-        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; });
-        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
-        __syncthreads();
+        group_sync<NTH>(g);
+        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        group_sync<NTH>(g);
         float s[4][4];
         tile_dot<DK>(sQ, sK, ty, tx, s);
 #pragma unroll
@@ -87,10 +128,36 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s[i][j] = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S) ? s[i][j] * scale_log2 : -INFINITY;
-        softmax_step<DV / 16>(s, m, l, acc);
+        softmax_step<N>(s, m, l, acc);
         put_tile(sP, ty, tx, s);
-        __syncthreads();
+        group_sync<NTH>(g);
         tile_mul<DV>(sP, sV, ty, tx, acc);
+    }
+    if (NG > 1) {
+        __syncthreads();
+        if (g > 0) {
+            put_sums<N>(mine, tid, acc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mine[(4 * N + i) * NTH + tid] = m[i];
+                mine[(4 * N + 4 + i) * NTH + tid] = l[i];
+            }
+        }
+        __syncthreads();
+        if (g > 0) return;
+        for (int x = 1; x < NG; ++x) {
+            const float* w = mine + x * Fwd<DK, DV>::each;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float mx = w[(4 * N + i) * NTH + tid], lx = w[(4 * N + 4 + i) * NTH + tid];
+                const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+                const float a0 = exp2f(m[i] - base), a1 = exp2f(mx - base);
+                m[i] = mn;
+                l[i] = fmaf(l[i], a0, lx * a1);
+#pragma unroll
+                for (int c = 0; c < N; ++c) acc[i][c] = fmaf(acc[i][c], a0, w[(i * N + c) * NTH + tid] * a1);
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -98,39 +165,38 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
         if (t >= T) continue;
         const float inv = 1.f / l[i];
 #pragma unroll
-        for (int c = 0; c < DV / 16; ++c)
+        for (int c = 0; c < N; ++c)
             store1_as(o, bf16, (bh * T + t) * (int64_t)DV + Cols<DV>::at(tx, c), acc[i][c] * inv);
         if (tx == 0) lse[bh * T + t] = (m[i] + log2f(l[i])) * kLn2;
     }
 }
 
-template <int DK, int DV, int BQ>
-constexpr int dq_smem() { return (BQ * (ld<DK>() + ld<DV>()) + BK * (ld<DK>() + ld<DV>()) + BQ * LDP) * 4; }
-
 // With bf16 rows D from the stored o is off by about 2^-9 of it, which a row whose attention is peaked
 // turns into a larger error of dS = p (dP - D): there D0 from o only centres the sums, and
 //   e = sum_j p_j (dP_j - D0),  dq = scale (sum_j p_j (dP_j - D0) k_j - e sum_j p_j k_j),  D = D0 + e
 // gives the row's own D in the same pass, for one more product per tile.
-template <int DK, int DV, int BQ, bool BF16>
-__global__ void __launch_bounds__(4 * BQ)
+template <int DK, int DV, bool BF16>
+__global__ void __launch_bounds__(NTH * Dq<DK, DV>::NG)
 sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                const void* __restrict__ o, const float* __restrict__ lse, const void* __restrict__ dO,
                void* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     constexpr bool bf16 = BF16;
-    constexpr int NTH = 4 * BQ;
+    constexpr int NG = Dq<DK, DV>::NG;
     extern __shared__ __align__(16) float sm[];
+    const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sQ = sm;
     float* sG = sQ + BQ * ld<DK>();
-    float* sK = sG + BQ * ld<DV>();
+    float* mine = sm + Dq<DK, DV>::own + g0 * Dq<DK, DV>::each;
+    float* sK = mine;
     float* sV = sK + BK * ld<DK>();
     float* sP = sV + BK * ld<DV>();
     const int64_t bh = blockIdx.x / qtiles, b = bh / H;
     const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
     const float scale_log2 = scale * kLog2e;
-    load_tile<DK, BQ, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
-    load_tile<DV, BQ, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
+    load_tile<DK, BQ, NTH * NG>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    load_tile<DV, BQ, NTH * NG>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
     __syncthreads();
     float L2[4], D[4], e[4], acc[4][DK / 16], pk[4][BF16 ? DK / 16 : 1];
 #pragma unroll
@@ -146,7 +212,7 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
             }
         D[i] = row_sum(d);
         L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
-        if (!BF16 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
+        if (!BF16 && g0 == 0 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c) {
             acc[i][c] = 0.f;
@@ -154,12 +220,12 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
         }
     }
     const KeyTiles kt = key_tiles(t0, t1, W, S);
-    for (int it = 0; it < kt.n; ++it) {
+    for (int it = g0; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
-        __syncthreads();
-        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; });
-        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
-        __syncthreads();
+        group_sync<NTH>(g0);
+        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        group_sync<NTH>(g0);
         float s[4][4], g[4][4];
         tile_dot<DK>(sQ, sK, ty, tx, s);
         tile_dot<DV>(sG, sV, ty, tx, g);
@@ -173,13 +239,35 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
                 e[i] += g[i][j];
             }
         put_tile(sP, ty, tx, g);
-        __syncthreads();
+        group_sync<NTH>(g0);
         tile_mul<DK>(sP, sK, ty, tx, acc);
         if constexpr (BF16) {
-            __syncthreads();
+            group_sync<NTH>(g0);
             put_tile(sP, ty, tx, s);
-            __syncthreads();
+            group_sync<NTH>(g0);
             tile_mul<DK>(sP, sK, ty, tx, pk);
+        }
+    }
+    if (NG > 1) {
+        __syncthreads();
+        if (g0 > 0) {
+            put_sums<DK / 16>(mine, tid, acc);
+            if constexpr (BF16) {
+                put_sums<DK / 16>(mine + 4 * (DK / 16) * NTH, tid, pk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mine[(8 * (DK / 16) + i) * NTH + tid] = e[i];
+            }
+        }
+        __syncthreads();
+        if (g0 > 0) return;
+        for (int x = 1; x < NG; ++x) {
+            const float* w = mine + x * Dq<DK, DV>::each;
+            add_sums<DK / 16>(w, tid, acc);
+            if constexpr (BF16) {
+                add_sums<DK / 16>(w + 4 * (DK / 16) * NTH, tid, pk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] += w[(8 * (DK / 16) + i) * NTH + tid];
+            }
         }
     }
 #pragma unroll
@@ -198,33 +286,31 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
     }
 }
 
-template <int DK, int DV, int BQ>
-constexpr int dkv_smem() {
-    return ((BQ + BK) * (ld<DK>() + ld<DV>()) + BQ * LDP + 2 * BK) * 4;
-}
-
 // blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
-template <int DK, int DV, int BQ>
-__global__ void __launch_bounds__(4 * BQ)
+template <int DK, int DV>
+__global__ void __launch_bounds__(NTH * Dkv<DK, DV>::NG)
 sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
                 const float* __restrict__ lse, const float* __restrict__ dbuf, const void* __restrict__ dO,
                 void* __restrict__ dv, SinkParts parts, bool bf16, int B, int H, int T, int W, int S, float scale) {
-    constexpr int NTH = 4 * BQ;
+    constexpr int NG = Dkv<DK, DV>::NG;
     extern __shared__ __align__(16) float sm[];
+    const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sK = sm;
     float* sV = sK + BQ * ld<DK>();
-    float* sQ = sV + BQ * ld<DV>();
+    float* mine = sm + Dkv<DK, DV>::own + g0 * Dkv<DK, DV>::each;
+    float* sQ = mine;
     float* sG = sQ + BK * ld<DK>();
     float* sP = sG + BK * ld<DV>();
     float* sL = sP + BQ * LDP;
     float* sD = sL + BK;
     const int h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = (int64_t)b * H + h;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int tx = tid % 16, ty = tid / 16;
     const SinkWork w = parts.work((int)blockIdx.x);
     const int key0 = w.tile * BQ;
-    load_tile<DK, BQ, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
-    load_tile<DV, BQ, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    load_tile<DK, BQ, NTH * NG>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
+    load_tile<DV, BQ, NTH * NG>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    __syncthreads();
     const float scale_log2 = scale * kLog2e;
     float ak[4][DK / 16], av[4][DV / 16];
 #pragma unroll
@@ -234,16 +320,16 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
 #pragma unroll
         for (int c = 0; c < DV / 16; ++c) av[i][c] = 0.f;
     }
-    for (int qt = w.q_lo; qt <= w.q_hi; ++qt) {
+    for (int qt = w.q_lo + g0; qt <= w.q_hi; qt += NG) {
         const int t0 = qt * BK;
-        __syncthreads();
-        load_tile<DK, BK, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
-        load_tile<DV, BK, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
-        for (int r = threadIdx.x; r < BK; r += NTH) {
+        group_sync<NTH>(g0);
+        load_tile<DK, BK, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; }, tid);
+        for (int r = tid; r < BK; r += NTH) {
             sL[r] = t0 + r < T ? lse[bh * T + t0 + r] * kLog2e : INFINITY;
             sD[r] = t0 + r < T ? dbuf[bh * T + t0 + r] : 0.f;
         }
-        __syncthreads();
+        group_sync<NTH>(g0);
         float s[4][4], g[4][4];  // rows: keys, columns: queries
         tile_dot<DK>(sK, sQ, ty, tx, s);
         tile_dot<DV>(sV, sG, ty, tx, g);
@@ -257,12 +343,25 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
                 g[i][j] = s[i][j] * (g[i][j] - sD[c]);
             }
         put_tile(sP, ty, tx, s);
-        __syncthreads();
+        group_sync<NTH>(g0);
         tile_mul<DV>(sP, sG, ty, tx, av);
-        __syncthreads();
+        group_sync<NTH>(g0);
         put_tile(sP, ty, tx, g);
-        __syncthreads();
+        group_sync<NTH>(g0);
         tile_mul<DK>(sP, sQ, ty, tx, ak);
+    }
+    if (NG > 1) {
+        __syncthreads();
+        if (g0 > 0) {
+            put_sums<DK / 16>(mine, tid, ak);
+            put_sums<DV / 16>(mine + 4 * (DK / 16) * NTH, tid, av);
+        }
+        __syncthreads();
+        if (g0 > 0) return;
+        for (int x = 1; x < NG; ++x) {
+            add_sums<DK / 16>(mine + x * Dkv<DK, DV>::each, tid, ak);
+            add_sums<DV / 16>(mine + x * Dkv<DK, DV>::each + 4 * (DK / 16) * NTH, tid, av);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -284,68 +383,52 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     }
 }
 
-template <int DK, int DV, int BQ>
+template <int DK, int DV>
 cudaError_t fwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
-    constexpr int smem = fwd_smem<DK, DV, BQ>();
+    using F = Fwd<DK, DV>;
     const int qtiles = (a.T + BQ - 1) / BQ;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem);
     if (e != cudaSuccess) return e;
-    sink_fwd_kernel<DK, DV, BQ><<<(unsigned)grid, 4 * BQ, smem, s>>>(
+    sink_fwd_kernel<DK, DV><<<(unsigned)grid, NTH * F::NG, F::smem, s>>>(
         a.q, a.k, a.v, a.out, a.lse_out, bf16, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
     note_launches(1);
     return cudaGetLastError();
 }
 
-template <int DK, int DV, int BQ>
+template <int DK, int DV>
 cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
-    constexpr int q_smem = dq_smem<DK, DV, BQ>(), kv_smem = dkv_smem<DK, DV, BQ>();
+    using Q = Dq<DK, DV>;
+    using K = Dkv<DK, DV>;
     const int qtiles = (a.T + BQ - 1) / BQ;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL || a.B > 65535) return cudaErrorInvalidConfiguration;
     SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, BQ, true> : sink_dq_kernel<DK, DV, BQ, false>;
-    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem)) != cudaSuccess)
+    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, true> : sink_dq_kernel<DK, DV, false>;
+    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::smem)) != cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem)) !=
+    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::smem)) !=
         cudaSuccess)
         return e;
-    dq_kernel<<<(unsigned)grid, 4 * BQ, q_smem, s>>>(a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W, a.S,
-                                                     a.scale, qtiles);
-    sink_dkv_kernel<DK, DV, BQ><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), 4 * BQ, kv_smem, s>>>(
+    dq_kernel<<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W,
+                                                          a.S, a.scale, qtiles);
+    sink_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH * K::NG, K::smem, s>>>(
         a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H, a.T, a.W, a.S, a.scale);
     note_launches(2);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, bf16, s);
 }
 
-// rows per CTA: the most that still gives every SM work
-int rows_for(int B, int H, int T) {
-    const int64_t want = device_sm_count();
-    for (int rows = 64; rows > 16; rows /= 2)
-        if ((int64_t)B * H * ((T + rows - 1) / rows) >= want) return rows;
-    return 16;
-}
-
-template <int DK, int DV>
-cudaError_t pick_rows(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
-    switch (rows_for(a.B, a.H, a.T)) {
-        case 64: return backward ? bwd_t<DK, DV, 64>(a, bf16, s) : fwd_t<DK, DV, 64>(a, bf16, s);
-        case 32: return backward ? bwd_t<DK, DV, 32>(a, bf16, s) : fwd_t<DK, DV, 32>(a, bf16, s);
-        default: return backward ? bwd_t<DK, DV, 16>(a, bf16, s) : fwd_t<DK, DV, 16>(a, bf16, s);
-    }
-}
-
 template <int DK>
 cudaError_t pick_dv(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
     switch (a.d_v) {
-        case 16: return pick_rows<DK, 16>(a, bf16, backward, s);
-        case 32: return pick_rows<DK, 32>(a, bf16, backward, s);
-        case 64: return pick_rows<DK, 64>(a, bf16, backward, s);
-        case 128: return pick_rows<DK, 128>(a, bf16, backward, s);
+        case 16: return backward ? bwd_t<DK, 16>(a, bf16, s) : fwd_t<DK, 16>(a, bf16, s);
+        case 32: return backward ? bwd_t<DK, 32>(a, bf16, s) : fwd_t<DK, 32>(a, bf16, s);
+        case 64: return backward ? bwd_t<DK, 64>(a, bf16, s) : fwd_t<DK, 64>(a, bf16, s);
+        case 128: return backward ? bwd_t<DK, 128>(a, bf16, s) : fwd_t<DK, 128>(a, bf16, s);
     }
     return cudaErrorInvalidValue;
 }
