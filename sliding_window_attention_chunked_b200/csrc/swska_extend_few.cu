@@ -19,10 +19,17 @@
 #include <math.h>
 
 #include "extend.cuh"
+#include "mma16.cuh"
 #include "tc.cuh"
 
 namespace rod {
 namespace {
+
+using mma::bits_from;
+using mma::bits_to;
+using mma::ldsm4;
+using mma::ldsm4t;
+using mma::mma16816;
 
 __device__ unsigned int g_extend_few_timeout = 0;
 
@@ -54,20 +61,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
     }
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
 // 16-byte chunk c (of 16) of row r of the key tile: two halves of 64 columns, swizzled
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -78,10 +71,6 @@ __device__ __forceinline__ uint32_t rows_at(int rg, int head, int hpg, int box) 
     const int per = box / 8;
     return (uint32_t)(((rg / per * hpg + head) * per + rg % per) * 1024);
 }
-
-// bits 0 .. x and bits x .. 31 of a word, for any x
-__device__ __forceinline__ uint32_t bits_to(int x) { return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u); }
-__device__ __forceinline__ uint32_t bits_from(int64_t x) { return x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x); }
 
 __global__ void __launch_bounds__(NTH, 1)
 extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,

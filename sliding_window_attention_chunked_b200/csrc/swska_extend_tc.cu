@@ -21,10 +21,14 @@
 #include <math.h>
 
 #include "extend.cuh"
+#include "mma16.cuh"
 #include "tc.cuh"
 
 namespace rod {
 namespace {
+
+using mma::bits_from;
+using mma::bits_to;
 
 __device__ unsigned int g_extend_tc_timeout = 0;
 
@@ -84,10 +88,6 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-
-// bits 0 .. x and bits x .. 31 of a word, for any x
-__device__ __forceinline__ uint32_t bits_to(int x) { return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u); }
-__device__ __forceinline__ uint32_t bits_from(int64_t x) { return x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x); }
 
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

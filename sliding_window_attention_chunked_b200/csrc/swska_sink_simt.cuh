@@ -1,5 +1,5 @@
-// swska_sink_simt.cuh -- SW-SKA with first tokens that stay visible, forward and backward on CUDA
-// cores (every product an fp32 FMA): fp32 inputs, and bf16 shapes outside the tensor-core kernels.
+// swska_sink_simt.cuh -- SW-SKA with first tokens that stay visible, forward and backward in fp32 on
+// CUDA cores (every product an fp32 FMA).
 //
 // Query t sees the keys j <= t with j > t - W or j < S:
 //   p_tj = softmax_j(scale q_t . k_j),  o_t = sum_j p_tj v_j,  lse_t = log sum_j exp(scale q_t . k_j)
@@ -89,8 +89,8 @@ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int W, int S) {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Fwd<DK, DV>::NG)
-sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
-                void* __restrict__ o, float* __restrict__ lse, bool bf16, int H, int T, int W, int S, float scale_log2,
+sink_fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                float* __restrict__ o, float* __restrict__ lse, int H, int T, int W, int S, float scale_log2,
                 int qtiles) {
     constexpr int NG = Fwd<DK, DV>::NG, N = DV / 16;
     extern __shared__ __align__(16) float sm[];
@@ -104,7 +104,7 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
     const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
-    load_tile<DK, BQ, NTH * NG>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    load_tile<DK, BQ, NTH * NG>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
     __syncthreads();
     const KeyTiles kt = key_tiles(t0, t1, W, S);
     float m[4], l[4], acc[4][N];
@@ -118,8 +118,8 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     for (int it = g; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
         group_sync<NTH>(g);
-        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        load_tile<DK, BK, NTH>(sK, k, false, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
         group_sync<NTH>(g);
         float s[4][4];
         tile_dot<DK>(sQ, sK, ty, tx, s);
@@ -166,21 +166,16 @@ sink_fwd_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
         const float inv = 1.f / l[i];
 #pragma unroll
         for (int c = 0; c < N; ++c)
-            store1_as(o, bf16, (bh * T + t) * (int64_t)DV + Cols<DV>::at(tx, c), acc[i][c] * inv);
+            o[(bh * T + t) * (int64_t)DV + Cols<DV>::at(tx, c)] = acc[i][c] * inv;
         if (tx == 0) lse[bh * T + t] = (m[i] + log2f(l[i])) * kLn2;
     }
 }
 
-// With bf16 rows D from the stored o is off by about 2^-9 of it, which a row whose attention is peaked
-// turns into a larger error of dS = p (dP - D): there D0 from o only centres the sums, and
-//   e = sum_j p_j (dP_j - D0),  dq = scale (sum_j p_j (dP_j - D0) k_j - e sum_j p_j k_j),  D = D0 + e
-// gives the row's own D in the same pass, for one more product per tile.
-template <int DK, int DV, bool BF16>
+template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dq<DK, DV>::NG)
-sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
-               const void* __restrict__ o, const float* __restrict__ lse, const void* __restrict__ dO,
-               void* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
-    constexpr bool bf16 = BF16;
+sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+               const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ dO,
+               float* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     constexpr int NG = Dq<DK, DV>::NG;
     extern __shared__ __align__(16) float sm[];
     const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
@@ -195,36 +190,31 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
     const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
     const float scale_log2 = scale * kLog2e;
-    load_tile<DK, BQ, NTH * NG>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
-    load_tile<DV, BQ, NTH * NG>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
+    load_tile<DK, BQ, NTH * NG>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
+    load_tile<DV, BQ, NTH * NG>(sG, dO, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
     __syncthreads();
-    float L2[4], D[4], e[4], acc[4][DK / 16], pk[4][BF16 ? DK / 16 : 1];
+    float L2[4], D[4], acc[4][DK / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, t = t0 + r;
-        e[i] = 0.f;
         float d = 0.f;
         if (t < T)
             for (int c = tx; c < DV; c += 16) {
                 const int64_t at = (bh * T + t) * (int64_t)DV + c;
-                const float ov = bf16 ? to_f32(static_cast<const __nv_bfloat16*>(o)[at]) : static_cast<const float*>(o)[at];
-                d = fmaf(sG[r * ld<DV>() + c], ov, d);
+                d = fmaf(sG[r * ld<DV>() + c], o[at], d);
             }
         D[i] = row_sum(d);
         L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
-        if (!BF16 && g0 == 0 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
+        if (g0 == 0 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
 #pragma unroll
-        for (int c = 0; c < DK / 16; ++c) {
-            acc[i][c] = 0.f;
-            if (BF16) pk[i][c] = 0.f;
-        }
+        for (int c = 0; c < DK / 16; ++c) acc[i][c] = 0.f;
     }
     const KeyTiles kt = key_tiles(t0, t1, W, S);
     for (int it = g0; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
         group_sync<NTH>(g0);
-        load_tile<DK, BK, NTH>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        load_tile<DK, BK, NTH>(sK, k, false, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
         group_sync<NTH>(g0);
         float s[4][4], g[4][4];
         tile_dot<DK>(sQ, sK, ty, tx, s);
@@ -234,64 +224,40 @@ sink_dq_kernel(const void* __restrict__ q, const void* __restrict__ k, const voi
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool see = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S);
-                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) : 0.f;
-                g[i][j] = s[i][j] * (g[i][j] - D[i]);
-                e[i] += g[i][j];
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) * (g[i][j] - D[i]) : 0.f;
             }
-        put_tile(sP, ty, tx, g);
+        put_tile(sP, ty, tx, s);
         group_sync<NTH>(g0);
         tile_mul<DK>(sP, sK, ty, tx, acc);
-        if constexpr (BF16) {
-            group_sync<NTH>(g0);
-            put_tile(sP, ty, tx, s);
-            group_sync<NTH>(g0);
-            tile_mul<DK>(sP, sK, ty, tx, pk);
-        }
     }
     if (NG > 1) {
         __syncthreads();
         if (g0 > 0) {
             put_sums<DK / 16>(mine, tid, acc);
-            if constexpr (BF16) {
-                put_sums<DK / 16>(mine + 4 * (DK / 16) * NTH, tid, pk);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mine[(8 * (DK / 16) + i) * NTH + tid] = e[i];
-            }
         }
         __syncthreads();
         if (g0 > 0) return;
         for (int x = 1; x < NG; ++x) {
             const float* w = mine + x * Dq<DK, DV>::each;
             add_sums<DK / 16>(w, tid, acc);
-            if constexpr (BF16) {
-                add_sums<DK / 16>(w + 4 * (DK / 16) * NTH, tid, pk);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] += w[(8 * (DK / 16) + i) * NTH + tid];
-            }
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + 4 * ty + i;
-        if constexpr (BF16) {
-            const float er = row_sum(e[i]);
-#pragma unroll
-            for (int c = 0; c < DK / 16; ++c) acc[i][c] = fmaf(-er, pk[i][c], acc[i][c]);
-            if (tx == 0 && t < T) dbuf[bh * T + t] = D[i] + er;
-        }
         if (t >= T) continue;
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c)
-            store1_as(dq, bf16, (bh * T + t) * (int64_t)DK + Cols<DK>::at(tx, c), acc[i][c] * scale);
+            dq[(bh * T + t) * (int64_t)DK + Cols<DK>::at(tx, c)] = acc[i][c] * scale;
     }
 }
 
 // blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dkv<DK, DV>::NG)
-sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
-                const float* __restrict__ lse, const float* __restrict__ dbuf, const void* __restrict__ dO,
-                void* __restrict__ dv, SinkParts parts, bool bf16, int B, int H, int T, int W, int S, float scale) {
+sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                const float* __restrict__ lse, const float* __restrict__ dbuf, const float* __restrict__ dO,
+                float* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
     constexpr int NG = Dkv<DK, DV>::NG;
     extern __shared__ __align__(16) float sm[];
     const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
@@ -308,8 +274,8 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     const int tx = tid % 16, ty = tid / 16;
     const SinkWork w = parts.work((int)blockIdx.x);
     const int key0 = w.tile * BQ;
-    load_tile<DK, BQ, NTH * NG>(sK, k, bf16, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
-    load_tile<DV, BQ, NTH * NG>(sV, v, bf16, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    load_tile<DK, BQ, NTH * NG>(sK, k, false, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
+    load_tile<DV, BQ, NTH * NG>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
     __syncthreads();
     const float scale_log2 = scale * kLog2e;
     float ak[4][DK / 16], av[4][DV / 16];
@@ -323,8 +289,8 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     for (int qt = w.q_lo + g0; qt <= w.q_hi; qt += NG) {
         const int t0 = qt * BK;
         group_sync<NTH>(g0);
-        load_tile<DK, BK, NTH>(sQ, q, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sG, dO, bf16, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; }, tid);
+        load_tile<DK, BK, NTH>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; }, tid);
+        load_tile<DV, BK, NTH>(sG, dO, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; }, tid);
         for (int r = tid; r < BK; r += NTH) {
             sL[r] = t0 + r < T ? lse[bh * T + t0 + r] * kLog2e : INFINITY;
             sD[r] = t0 + r < T ? dbuf[bh * T + t0 + r] : 0.f;
@@ -372,7 +338,7 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
         for (int c = 0; c < DV / 16; ++c) {
             const int col = Cols<DV>::at(tx, c);
             if (part) parts.dv_at(w.slot, bh, key)[col] = av[i][c];
-            else if (w.slot == 0) store1_as(dv, bf16, (bh * T + key) * (int64_t)DV + col, av[i][c]);
+            else if (w.slot == 0) dv[(bh * T + key) * (int64_t)DV + col] = av[i][c];
         }
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c) {
@@ -383,8 +349,10 @@ sink_dkv_kernel(const void* __restrict__ q, const void* __restrict__ k, const vo
     }
 }
 
+const float* f32(const void* p) { return static_cast<const float*>(p); }
+
 template <int DK, int DV>
-cudaError_t fwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t fwd_t(const SinkArgs& a, cudaStream_t s) {
     using F = Fwd<DK, DV>;
     const int qtiles = (a.T + BQ - 1) / BQ;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
@@ -392,13 +360,13 @@ cudaError_t fwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem);
     if (e != cudaSuccess) return e;
     sink_fwd_kernel<DK, DV><<<(unsigned)grid, NTH * F::NG, F::smem, s>>>(
-        a.q, a.k, a.v, a.out, a.lse_out, bf16, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
+        f32(a.q), f32(a.k), f32(a.v), static_cast<float*>(a.out), a.lse_out, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
     note_launches(1);
     return cudaGetLastError();
 }
 
 template <int DK, int DV>
-cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     using Q = Dq<DK, DV>;
     using K = Dkv<DK, DV>;
     const int qtiles = (a.T + BQ - 1) / BQ;
@@ -407,28 +375,28 @@ cudaError_t bwd_t(const SinkArgs& a, bool bf16, cudaStream_t s) {
     SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    auto* dq_kernel = bf16 ? sink_dq_kernel<DK, DV, true> : sink_dq_kernel<DK, DV, false>;
+    auto* dq_kernel = sink_dq_kernel<DK, DV>;
     if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::smem)) != cudaSuccess)
         return e;
     if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::smem)) !=
         cudaSuccess)
         return e;
-    dq_kernel<<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(a.q, a.k, a.v, a.o, a.lse, a.dO, a.dq, dbuf, a.H, a.T, a.W,
-                                                          a.S, a.scale, qtiles);
+    dq_kernel<<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
+        f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
     sink_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH * K::NG, K::smem, s>>>(
-        a.q, a.k, a.v, a.lse, dbuf, a.dO, a.dv, parts, bf16, a.B, a.H, a.T, a.W, a.S, a.scale);
+        f32(a.q), f32(a.k), f32(a.v), a.lse, dbuf, f32(a.dO), static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
     note_launches(2);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return sink_parts_reduce(parts, a, bf16, s);
+    return sink_parts_reduce(parts, a, false, s);
 }
 
 template <int DK>
-cudaError_t pick_dv(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
+cudaError_t pick_dv(const SinkArgs& a, bool backward, cudaStream_t s) {
     switch (a.d_v) {
-        case 16: return backward ? bwd_t<DK, 16>(a, bf16, s) : fwd_t<DK, 16>(a, bf16, s);
-        case 32: return backward ? bwd_t<DK, 32>(a, bf16, s) : fwd_t<DK, 32>(a, bf16, s);
-        case 64: return backward ? bwd_t<DK, 64>(a, bf16, s) : fwd_t<DK, 64>(a, bf16, s);
-        case 128: return backward ? bwd_t<DK, 128>(a, bf16, s) : fwd_t<DK, 128>(a, bf16, s);
+        case 16: return backward ? bwd_t<DK, 16>(a, s) : fwd_t<DK, 16>(a, s);
+        case 32: return backward ? bwd_t<DK, 32>(a, s) : fwd_t<DK, 32>(a, s);
+        case 64: return backward ? bwd_t<DK, 64>(a, s) : fwd_t<DK, 64>(a, s);
+        case 128: return backward ? bwd_t<DK, 128>(a, s) : fwd_t<DK, 128>(a, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -438,6 +406,6 @@ cudaError_t pick_dv(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s)
 // forward or backward for one key head dim (an instance each in swska_sink_simt_<dk>.cu, which
 // compile side by side)
 template <int DK>
-cudaError_t sink_simt_launch(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s);
+cudaError_t sink_simt_launch(const SinkArgs& a, bool backward, cudaStream_t s);
 
 }  // namespace rod

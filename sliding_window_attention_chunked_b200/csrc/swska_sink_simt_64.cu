@@ -4,8 +4,8 @@
 namespace rod {
 
 template <>
-cudaError_t sink_simt_launch<64>(const SinkArgs& a, bool bf16, bool backward, cudaStream_t s) {
-    return pick_dv<64>(a, bf16, backward, s);
+cudaError_t sink_simt_launch<64>(const SinkArgs& a, bool backward, cudaStream_t s) {
+    return pick_dv<64>(a, backward, s);
 }
 
 }  // namespace rod
