@@ -9,6 +9,7 @@ namespace {
 // Memory bound: reads every part once, writes dk (and the S rows of dv) once.
 __global__ void __launch_bounds__(256)
 sink_reduce_kernel(const SinkParts p, void* __restrict__ dk, void* __restrict__ dv, bool bf16, float scale) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that made the parts
     const int64_t n_dk = (int64_t)p.B * p.T * p.dk / 4;
     const int64_t n_dv = p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_dk + n_dv;
@@ -60,9 +61,9 @@ SinkParts sink_parts_plan(const SinkArgs& a, int ks, int qs, int G) {
     const int near = SinkParts::near_hi(0, ks, qs, p.nq, a.W) + 1, far = p.nq - near;  // the first tile has the most
     if (p.R > 0 && far > 0) {
         p.n_tiles = (p.R + ks - 1) / ks;
-        // a segment is a window long, at least 4 tiles (its sums are S rows of memory traffic), and
-        // there are at most 64 of them
-        p.seg_len = near > 4 ? near : 4;
+        // a segment is no longer than a window, 4 to 8 tiles (short ones fill the end of the launch; each
+        // costs S rows of memory traffic), and there are at most 64 of them
+        p.seg_len = near > 4 ? (near < 8 ? near : 8) : 4;
         if (p.seg_len * 64 < far) p.seg_len = (far + 63) / 64;
         p.nseg = (far + p.seg_len - 1) / p.seg_len;
     }
@@ -87,9 +88,18 @@ float* sink_parts_bind(SinkParts& p, const SinkArgs& a) {
 cudaError_t sink_parts_reduce(const SinkParts& p, const SinkArgs& a, bool bf16, cudaStream_t s) {
     const int64_t n = (int64_t)p.B * p.T * p.dk / 4 + (p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0);
     const int64_t want = (n + 255) / 256, cap = 8 * (int64_t)device_sm_count();
-    sink_reduce_kernel<<<(unsigned)(want < cap ? want : cap), 256, 0, s>>>(p, a.dk, a.dv, bf16, a.scale);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(want < cap ? want : cap));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, sink_reduce_kernel, p, a.dk, a.dv, bf16, a.scale);
     note_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace rod

@@ -174,7 +174,9 @@ __device__ __forceinline__ uint32_t s_col(int u) { return (u & 1) ? 384u : 0u; }
 __device__ __forceinline__ uint32_t packed_col(int k) { return (uint32_t)(8 * k + (k >= 4 ? 32 : 0)); }
 
 // SINK: the first S tokens stay visible to every query; their key tile comes before the window's.
-// There D = dbuf comes from the stored bf16 o, off by about 2^-9 of it. Where a row's attention is
+// There D = dbuf comes from the stored bf16 o, off by about 2^-9 of it. (Making the row statistics here
+// instead of in a launch of their own costs more: a CTA has the SM to itself, so their loads wait in
+// the open. T 8192, 16 heads: 946 us a step against 910.) Where a row's attention is
 // peaked, dS = p (dP - D) of the peak is a small difference and that error would show. So the sweep
 // also sums e = sum_j p_j (dP_j - D) of each row in fp32, D + e (the row's own sum p dP) goes back to
 // dbuf for the key-tile kernel, and a CTA with a row that has some p above 1/2 sweeps its tiles once
@@ -188,6 +190,8 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   float* __restrict__ dbuf, int T, int Tpad, int H, int W, float scale_log2,
                   float scale, int n_qtiles, int S_arg) {
     using namespace qa;
+    // the key-tile kernel may set itself up on SMs that fall free; it waits for this launch's end
+    if (SINK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -571,6 +575,10 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_holder;
+    if (SINK) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the query-tile kernel's statistics
+    }
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 8) {
@@ -984,12 +992,22 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     const float sl = a.scale * kLog2e;
     ska_bwd_dq_kernel<true><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM_SINK, stream>>>(
         mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S);
-    ska_bwd_dkdv_kernel<true><<<dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B),
-                                NTHREADS_KEY, ka::SMEM, stream>>>(
-        mq, mdo, mk, mv, nlse2, dbuf, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T, (int)Tpad, H, H / G, W,
-        sl, nqt, a.S, parts);
-    note_launches(3);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B);
+    cfg.blockDim = dim3(NTHREADS_KEY);
+    cfg.dynamicSmemBytes = ka::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const float *cl = nlse2, *cd = dbuf;
+    e = cudaLaunchKernelEx(&cfg, ska_bwd_dkdv_kernel<true>, mq, mdo, mk, mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv),
+                           parts.dk_part, B, T, (int)Tpad, H, H / G, W, sl, nqt, a.S, parts);
+    note_launches(3);
+    if (e != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, true, stream);
 }
 

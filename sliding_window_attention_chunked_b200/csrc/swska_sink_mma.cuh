@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(NTH)
 sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ dbuf, const bf16_t* __restrict__ dO,
                     bf16_t* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that adds the parts waits for the end
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
     const uint32_t sK = smem_u32(sm), sV = sK + tile_bytes<DK>(), stage = sK + STAGE;

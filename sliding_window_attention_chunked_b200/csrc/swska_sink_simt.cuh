@@ -259,6 +259,7 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
                 const float* __restrict__ lse, const float* __restrict__ dbuf, const float* __restrict__ dO,
                 float* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
     constexpr int NG = Dkv<DK, DV>::NG;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that adds the parts waits for the end
     extern __shared__ __align__(16) float sm[];
     const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sK = sm;
