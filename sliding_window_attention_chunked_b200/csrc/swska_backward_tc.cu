@@ -178,10 +178,11 @@ __device__ __forceinline__ uint32_t packed_col(int k) { return (uint32_t)(8 * k 
 // instead of in a launch of their own costs more: a CTA has the SM to itself, so their loads wait in
 // the open. T 8192, 16 heads: 946 us a step against 910.) Where a row's attention is
 // peaked, dS = p (dP - D) of the peak is a small difference and that error would show. So the sweep
-// also sums e = sum_j p_j (dP_j - D) of each row in fp32, D + e (the row's own sum p dP) goes back to
-// dbuf for the key-tile kernel, and a CTA with a row that has some p above 1/2 sweeps its tiles once
-// more with it. Rows that see few keys are such rows (the first tile, short windows: a sweep of few
-// tiles); with long windows only peaked ones are.
+// also sums e = sum_j p_j (dP_j - D) of each row in fp32, and D + e (the row's own sum p dP) goes back
+// to dbuf for the key-tile kernel. The tile of the first tokens, where attention with such tokens
+// peaks, comes last: its dS already uses D + e, its own share of e included. A CTA with a row that has
+// some p above 1/2 in another tile sweeps its tiles once more with D + e; the error that stays
+// otherwise is 2^-9 of D times the sum of several p k_j, below the rounding of dS.
 template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -203,7 +204,10 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int S = SINK ? S_arg : 0;
     const int n_sink = min((S + TILE - 1) / TILE, kt_lo);
     const int n_it = qt - kt_lo + 1 + n_sink;  // key tiles of the first tokens and of the window
-    auto key_tile = [&](int i) { return i < n_sink ? i : kt_lo + i - n_sink; };
+    auto key_tile = [&](int i) {
+        if (SINK) i = i + 1 < n_it ? i + 1 : 0;  // the first tile last
+        return i < n_sink ? i : kt_lo + i - n_sink;
+    };
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* kfull = bars;
@@ -414,6 +418,27 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // phase 2: dS = P (dP - D), packed over this half's first 32 columns of the S buffer
             if (!wait_bar_warp(pfull, (uint32_t)(u & 1), abort_flag)) { ok = false; break; }
             tc::fence_after_sync();
+            const bool last = SINK && u == n_it - 1;
+            if (last) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t dp[32];
+                    tc::tmem_ld32(tP + 32u * c, dp);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) e2 = f2fma(p2[16 * c + i], f2sub(raw2(dp, 2 * i), d2), e2);
+                }
+                float* sums = reinterpret_cast<float*>(smem + OFF_SUMS);
+                sums[TILE * w + row] = e2.x + e2.y;
+                if (t < T && p_max > 0.5f) *redo = 1;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                met = true;
+                Dr += sums[row] + sums[TILE + row];
+                d2 = make_float2(Dr, Dr);
+                if (w == 0 && t < T) dbuf[(int64_t)bh * Tpad + t] = Dr;
+                if (*redo) u_end = 2 * n_it;
+                if (threadIdx.x == 0) mbar_arrive(decided);
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t dp[32], pk[16];
@@ -433,18 +458,6 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             tc::tmem_wait_st();
             tc::fence_before_sync();
             mbar_arrive(dsready);
-            if (SINK && u == n_it - 1) {
-                float* sums = reinterpret_cast<float*>(smem + OFF_SUMS);
-                sums[TILE * w + row] = e2.x + e2.y;
-                if (t < T && p_max > 0.5f) *redo = 1;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                met = true;
-                Dr += sums[row] + sums[TILE + row];
-                d2 = make_float2(Dr, Dr);
-                if (w == 0 && t < T) dbuf[(int64_t)bh * Tpad + t] = Dr;
-                if (*redo) u_end = 2 * n_it;
-                if (threadIdx.x == 0) mbar_arrive(decided);
-            }
         }
         // a warp that gave up does not leave the others at the meeting
         if (SINK && !met) asm volatile("bar.sync 1, 256;" ::: "memory");

@@ -63,6 +63,42 @@ def test_training_step_long(dtype, T, W, S):
     _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"long {dtype} T{T}")
 
 
+@pytest.mark.parametrize("dtype,d,T,W,S,where", [("bf16", 128, 900, 300, 4, "first"), ("bf16", 128, 900, 300, 0, "window"), ("bf16", 128, 400, 1, 1, "first"),
+                                                 ("bf16", 64, 500, 100, 2, "first"), ("bf16", 32, 300, 90, 0, "window"), ("fp32", 64, 300, 90, 3, "first")])
+def test_gradients_where_attention_is_peaked(dtype, d, T, W, S, where):
+    """Rows that give one key nearly everything (a first token, or one in the window): dS = p (dP - D) is a small
+    difference there, so dq is held to the roundings of dS itself, with no allowance for an error of D beyond that of the
+    exponentials (2^-13 each): tolerance H |dq| + (2^-8 + 2^-13) sum p |dP - D| |k| scale + 2^-12 (sum p |dP - D|) (sum p |k|) scale, and
+    D's own sums in fp32, d 2^-22 (sum p |dO| |v|) (sum p |k|) scale."""
+    H = 2
+    q, k, v = wl.swska_inputs(1, H, T, d, d, seed=T, dtype=dtype, device=DEV)
+    u = torch.randn(d, device=DEV)
+    u /= u.norm()
+    at = torch.arange(T, device=DEV) % (T if where == "first" else W) == (0 if where == "first" else 7)
+    q = (q.float() + math.sqrt(d) * u).to(DT[dtype])
+    k = torch.where(at[None, :, None], k.float() + 11 * u, k.float()).to(DT[dtype])
+    dO = torch.randn_like(v)
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    t = torch.arange(T, device=DEV)
+    see, scale, half = ref.visible(t, t, W, S), d ** -0.5, torch.finfo(DT[dtype]).eps / 2
+    peaked = 0
+    for h in range(H):
+        Q, K, V, G = q[0, h].double(), k[0].double(), v[0, h].double(), dO[0, h].double()
+        o, _, p, _ = ref.attend(Q, K, V, see, scale)
+        dP = G @ V.T - (G * o).sum(1, keepdim=True)
+        want, a = (p * dP) @ K * scale, (p * dP.abs())
+        inner = (T + d) * 2.0 ** -23 * (1 + ref.amp(q, k)) + (2.0 ** -8 + 2.0 ** -13) * (dtype == "bf16")
+        tol = half * want.abs() * 1.01 + inner * (a @ K.abs()) * scale + (2.0 ** -12 if dtype == "bf16" else 2.0 ** -15) * a.sum(1, keepdim=True) * (p @ K.abs()) * scale + 1e-30
+        # D itself, the difference dP - D and the sums they come from are fp32: that error adds to the roundings of dS (a row that
+        # sees one key has dq = 0, and all that stands there is this)
+        tol += (d * 2.0 ** -22) * (G.abs() @ V.abs().T * p).sum(1, keepdim=True) * (p @ K.abs()) * scale
+        bad = (got["dq"][0, h].double() - want).abs() > tol
+        assert not bad.any(), f"head {h}: {int(bad.sum())} off at {bad.nonzero()[0].tolist()}"
+        peaked += int((p.max(1).values > 0.9).sum())
+    assert peaked > T // 4
+
+
 def test_training_step_scale_graph_and_streams():
     """An explicit scale; the step captured in a graph and replayed on new inputs equals the eager step bit for bit; so does
     one on a side stream, and a repeated one (no order of additions depends on timing)."""
