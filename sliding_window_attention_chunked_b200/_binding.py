@@ -510,10 +510,19 @@ def _expect(device, *items):
             raise ValueError(f"{name} is on {t.device}, the others on cuda:{device}")
 
 
+def _sizes(t, name, ndim):
+    """The shape of a tensor of ndim dims (checked in full by _expect)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != ndim:
+        _need(t, name, None, ndim)
+    return t.shape
+
+
 def _index(t, name):
     """The CUDA device index of the tensor that the others have to be with."""
-    _need(t, name)
-    return t.get_device()
+    dev = t.get_device()
+    if dev < 0:
+        _need(t, name)
+    return dev
 
 
 def _launch(device, stream, fn, *args):
@@ -546,16 +555,14 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
     """swska_prefill_lse whose first ``sinks`` tokens (0 .. 128) stay visible to every later query:
     q [B,H,T,dk], k [B,T,dk] (shared by the heads), v [B,H,T,dv]. Returns (o [B,H,T,dv],
     lse [B,H,T] fp32), the pair swska_sink_backward takes."""
+    B, H, T, dk = _sizes(q, "q", 4)
+    dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
-    _need(q, "q", None, 4)
-    _need(v, "v", dt, 4)
-    B, H, T, dk = q.shape
-    dv = v.shape[-1]
     if o is None:
         o = torch.empty((B, H, T, dv), dtype=dt, device=q.device)
     if lse is None:
         lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    _expect(dev, ("k", k, dt, (B, T, dk)), ("v", v, dt, (B, H, T, dv)), ("o", o, dt, (B, H, T, dv)),
+    _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, (B, H, T, dv)), ("o", o, dt, (B, H, T, dv)),
             ("lse", lse, torch.float32, (B, H, T)))
     _raise_on("rod_swska_sink_prefill",
               _launch(dev, stream, load_library().rod_swska_sink_prefill, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -567,13 +574,11 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
 def swska_sink_backward(q, k, v, o, lse, dO, window, sinks, scale=None, workspace=None, stream=None):
     """Gradients of swska_sink_prefill from its o and lse (same q, k, v, window, sinks and scale) and
     the loss gradient dO [B,H,T,dv]. Returns (dq, dk, dv) in the layouts and dtype of q, k, v."""
+    B, H, T, dk = _sizes(q, "q", 4)
+    dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
-    _need(q, "q", None, 4)
-    _need(v, "v", dt, 4)
-    B, H, T, dk = q.shape
-    dv = v.shape[-1]
     rows = (B, H, T, dv)
-    _expect(dev, ("k", k, dt, (B, T, dk)), ("v", v, dt, rows), ("o", o, dt, rows), ("dO", dO, dt, rows),
+    _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, rows), ("o", o, dt, rows), ("dO", dO, dt, rows),
             ("lse", lse, torch.float32, (B, H, T)))
     code, window, sinks = _dtype_code(q), int(window), int(sinks)
     ws = _workspace(workspace, dev, "rod_swska_sink_backward_workspace_size", B, H, T, dk, dv, window, sinks)
@@ -597,16 +602,13 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     j < sinks. max_len: a bound on the new tokens of one sequence (default M). k_new, v_new and
     slot_map may all be None: the cache has the tokens. Returns o [M,H,dv]; rows past
     cu_seqlens[N] are not written. The tables come from swska_page_tables."""
+    M, H, dk = _sizes(q, "q", 3)
+    P, _, page, dv = _sizes(v_pool, "v_pool", 4)
+    N, max_pages = _sizes(block_table, "block_table", 2)
     dev, dt = _index(q, "q"), q.dtype
-    _need(q, "q", None, 3)
-    _need(v_pool, "v_pool", dt, 4)
-    _need(block_table, "block_table", torch.int32, 2)
-    M, H, dk = q.shape
-    P, _, page, dv = v_pool.shape
-    N, max_pages = block_table.shape
     if o is None:
         o = torch.empty((M, H, dv), dtype=dt, device=q.device)
-    _expect(dev, ("k_pool", k_pool, dt, (P, page, dk)), ("v_pool", v_pool, dt, (P, H, page, dv)),
+    _expect(dev, ("q", q, dt, (M, H, dk)), ("k_pool", k_pool, dt, (P, page, dk)), ("v_pool", v_pool, dt, (P, H, page, dv)),
             ("block_table", block_table, torch.int32, (N, max_pages)), ("ctx", ctx, torch.int64, (N,)),
             ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,)), ("o", o, dt, (M, H, dv)))
     if k_new is not None and v_new is not None and slot_map is not None:
@@ -640,11 +642,10 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     (past the first ``sinks`` tokens) go back to the free list, pages for the new tokens are taken
     from it. Returns (cu_seqlens [N+1], slot_map [max_tokens]) int32 for swska_extend_paged; a
     sequence for which pages or tokens run out is served none this step."""
+    N, max_pages = _sizes(block_table, "block_table", 2)
+    P, M = _sizes(free_list, "free_list", 1)[0], int(max_tokens)
+    _sizes(ctx, "ctx", 1)
     dev, i32 = _index(ctx, "ctx"), torch.int32
-    _need(block_table, "block_table", i32, 2)
-    _need(free_list, "free_list", i32, 1)
-    N, max_pages = block_table.shape
-    P, M = free_list.shape[0], int(max_tokens)
     if M < 0:
         raise ValueError("max_tokens must not be negative")
     if cu_seqlens is None:

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace rod {
 
 // host-side count of kernel launches enqueued by this library (reported by rod_launch_count)
@@ -144,6 +146,9 @@ cudaError_t swska_cache_fill_launch(const void* k, const void* v, void* k_cache,
 // ---- SW-SKA with first tokens that stay visible ------------------------------------------------
 // streaming multiprocessors of the current device (queried once per device)
 int device_sm_count();
+// allows a kernel `bytes` of dynamic shared memory on the current device, once per device: `done` is
+// the caller's, one per kernel
+cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes);
 
 // forward (out, lse_out) or backward (o, lse, dO -> dq, dk, dv): query t sees the keys j <= t with
 // j > t - W or j < S

@@ -21,6 +21,17 @@ int device_sm_count() {
     cache[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
+
+cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 }  // namespace rod
 
 namespace {

@@ -995,12 +995,9 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     if ((e = make_tmap_bf16_3d(&mdo, a.dO, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mk, a.k, HD, (uint64_t)T, (uint64_t)B, 64, TILE)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mv, a.v, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(ska_bwd_dq_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  qa::SMEM_SINK)) != cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(ska_bwd_dkdv_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  ka::SMEM)) != cudaSuccess)
-        return e;
+    static std::atomic<uint64_t> q_set{0}, k_set{0};
+    if ((e = allow_smem(q_set, (const void*)ska_bwd_dq_kernel<true>, qa::SMEM_SINK)) != cudaSuccess) return e;
+    if ((e = allow_smem(k_set, (const void*)ska_bwd_dkdv_kernel<true>, ka::SMEM)) != cudaSuccess) return e;
     const int nqt = (int)(Tpad / TILE);
     const float sl = a.scale * kLog2e;
     ska_bwd_dq_kernel<true><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM_SINK, stream>>>(

@@ -436,7 +436,8 @@ cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, c
         return e;
     int stages = RING / (TILE * (1 + hpg));
     if (stages > MAXST) stages = MAXST;
-    if ((e = cudaFuncSetAttribute(extend_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> smem_set{0};
+    if ((e = allow_smem(smem_set, (const void*)extend_few_kernel, SMEM)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(r.cols * r.groups));  // one CTA per SM
     cfg.blockDim = dim3(NTH);

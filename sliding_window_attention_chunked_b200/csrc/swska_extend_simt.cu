@@ -133,7 +133,8 @@ extend_simt_kernel(const ExtendArgs a, const ExtendRoute r, bool bf16, float sca
 template <int DK, int DV, int BQ>
 cudaError_t launch_t(const ExtendArgs& a, const ExtendRoute& r, bool bf16, cudaStream_t s) {
     constexpr int smem = smem_bytes<DK, DV, BQ>();
-    cudaError_t e = cudaFuncSetAttribute(extend_simt_kernel<DK, DV, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, (const void*)extend_simt_kernel<DK, DV, BQ>, smem);
     if (e != cudaSuccess) return e;
     extend_simt_kernel<DK, DV, BQ><<<(unsigned)(r.cols * r.groups), 4 * BQ, smem, s>>>(
         a, r, bf16, a.scale * 1.4426950408889634f);

@@ -534,8 +534,8 @@ cudaError_t swska_extend_tc_launch(const ExtendArgs& a, const ExtendRoute& r, cu
     if ((e = make_tmap_bf16_3d(&mk, a.k_pool, HD, (uint64_t)a.page, (uint64_t)a.P, 64, (uint32_t)box)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mv, a.v_pool, HD, (uint64_t)a.page, (uint64_t)a.P * a.H, 64, (uint32_t)box)) != cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(extend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) != cudaSuccess)
-        return e;
+    static std::atomic<uint64_t> smem_set{0};
+    if ((e = allow_smem(smem_set, (const void*)extend_tc_kernel, SMEM_BYTES)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(r.cols * r.groups));  // one CTA per SM
     cfg.blockDim = dim3(NTHREADS);

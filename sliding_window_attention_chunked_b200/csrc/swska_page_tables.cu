@@ -377,8 +377,10 @@ cudaError_t swska_page_tables_launch(const int64_t* ctx, const int32_t* n_new, i
     const int CL = N <= NW && M <= 4 * NT ? 1 : kClusterMax;
     const int per = (N + CL - 1) / CL;
     const size_t smem = ((size_t)10 * per + 2 * (size_t)N + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    static std::atomic<uint64_t> smem_set{0};
+    constexpr int kMost = (10 * (kMaxTableSeqs / kClusterMax) + 2 * kMaxTableSeqs + 1) * (int)sizeof(int32_t);
+    static_assert(kMost <= 220 * 1024, "shared memory");
+    cudaError_t e = allow_smem(smem_set, (const void*)page_tables_kernel, kMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL);

@@ -422,7 +422,8 @@ cudaError_t fwd_t(const SinkArgs& a, cudaStream_t s) {
     const int qtiles = (a.T + R - 1) / R;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(sink_mma_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, (const void*)sink_mma_fwd_kernel<DK, DV>, smem);
     if (e != cudaSuccess) return e;
     sink_mma_fwd_kernel<DK, DV><<<(unsigned)grid, NTH, smem, s>>>(
         static_cast<const bf16_t*>(a.q), static_cast<const bf16_t*>(a.k), static_cast<const bf16_t*>(a.v),
@@ -440,10 +441,9 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     SinkParts parts = sink_parts_plan(a, R, R, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(sink_mma_dq_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem)) != cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(sink_mma_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem)) != cudaSuccess)
-        return e;
+    static std::atomic<uint64_t> q_set{0}, k_set{0};
+    if ((e = allow_smem(q_set, (const void*)sink_mma_dq_kernel<DK, DV>, q_smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(k_set, (const void*)sink_mma_dkv_kernel<DK, DV>, kv_smem)) != cudaSuccess) return e;
     const bf16_t *q = static_cast<const bf16_t*>(a.q), *k = static_cast<const bf16_t*>(a.k), *v = static_cast<const bf16_t*>(a.v),
                  *dO = static_cast<const bf16_t*>(a.dO);
     sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,

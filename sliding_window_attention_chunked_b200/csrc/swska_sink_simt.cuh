@@ -358,7 +358,8 @@ cudaError_t fwd_t(const SinkArgs& a, cudaStream_t s) {
     const int qtiles = (a.T + BQ - 1) / BQ;
     const int64_t grid = (int64_t)qtiles * a.B * a.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(sink_fwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, (const void*)sink_fwd_kernel<DK, DV>, F::smem);
     if (e != cudaSuccess) return e;
     sink_fwd_kernel<DK, DV><<<(unsigned)grid, NTH * F::NG, F::smem, s>>>(
         f32(a.q), f32(a.k), f32(a.v), static_cast<float*>(a.out), a.lse_out, a.H, a.T, a.W, a.S, a.scale * kLog2e, qtiles);
@@ -376,13 +377,10 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
     cudaError_t e;
-    auto* dq_kernel = sink_dq_kernel<DK, DV>;
-    if ((e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::smem)) != cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(sink_dkv_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::smem)) !=
-        cudaSuccess)
-        return e;
-    dq_kernel<<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
+    static std::atomic<uint64_t> q_set{0}, k_set{0};
+    if ((e = allow_smem(q_set, (const void*)sink_dq_kernel<DK, DV>, Q::smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(k_set, (const void*)sink_dkv_kernel<DK, DV>, K::smem)) != cudaSuccess) return e;
+    sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
         f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
     sink_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH * K::NG, K::smem, s>>>(
         f32(a.q), f32(a.k), f32(a.v), a.lse, dbuf, f32(a.dO), static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);

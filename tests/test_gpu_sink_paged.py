@@ -69,9 +69,11 @@ def test_gradients_where_attention_is_peaked(dtype, d, T, W, S, where):
     """Rows that give one key nearly everything (a first token, or one in the window): dS = p (dP - D) is a small
     difference there, so dq is held to the roundings of dS itself, with no allowance for an error of D beyond that of the
     exponentials (2^-13 each): tolerance H |dq| + (2^-8 + 2^-13) sum p |dP - D| |k| scale + 2^-12 (sum p |dP - D|) (sum p |k|) scale, and
-    D's own sums in fp32, d 2^-22 (sum p |dO| |v|) (sum p |k|) scale."""
+    D's own sums in fp32, d 2^-22 (sum p |dO| |v|) (sum p |k|) scale. The tcgen05 kernel takes D from the rounded o (off by 2^-8 of
+    |dO| |o|) for the keys other than the peak: 2^-8 (|dO| |o|) (sum of p |k| without the largest p) scale more."""
     H = 2
     q, k, v = wl.swska_inputs(1, H, T, d, d, seed=T, dtype=dtype, device=DEV)
+    torch.manual_seed(T + W)
     u = torch.randn(d, device=DEV)
     u /= u.norm()
     at = torch.arange(T, device=DEV) % (T if where == "first" else W) == (0 if where == "first" else 7)
@@ -93,6 +95,9 @@ def test_gradients_where_attention_is_peaked(dtype, d, T, W, S, where):
         # D itself, the difference dP - D and the sums they come from are fp32: that error adds to the roundings of dS (a row that
         # sees one key has dq = 0, and all that stands there is this)
         tol += (d * 2.0 ** -22) * (G.abs() @ V.abs().T * p).sum(1, keepdim=True) * (p @ K.abs()) * scale
+        if dtype == "bf16" and d == 128:
+            rest = torch.where(p == p.max(1, keepdim=True).values, 0, p)
+            tol += 2.0 ** -8 * (G * o).abs().sum(1, keepdim=True) * (rest @ K.abs()) * scale
         bad = (got["dq"][0, h].double() - want).abs() > tol
         assert not bad.any(), f"head {h}: {int(bad.sum())} off at {bad.nonzero()[0].tolist()}"
         peaked += int((p.max(1).values > 0.9).sum())
