@@ -31,7 +31,7 @@ namespace {
 
 constexpr int NT = 1024;
 constexpr int NW = NT / 32;
-constexpr int kClusterMax = 8;
+constexpr int kClusterMax = 16;  // opt-in: 8 is the portable size
 
 struct Sums {
     long long rel, need, tok;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
     __shared__ long long s_tot2[2];     // pages taken and tokens served, of the second
     __shared__ int s_done[NT];          // finished sequences of this CTA, while they fit
     __shared__ int s_ndone;
-    __shared__ int s_held[NW];
+    __shared__ int s_held[4][NW];
 
     int count0 = *a.free_count;
     count0 = count0 < 0 ? 0 : (count0 > a.P ? a.P : count0);
@@ -267,28 +267,30 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
         long long at = count0 + before.rel + s_relat[s_done[d]];
         for (int p0 = 0; p0 < a.max_pages; p0 += 4 * NT) {
             int32_t e[4];
-            bool some = false;
+            unsigned who[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int p = p0 + k * NT + (int)threadIdx.x;
                 e[k] = p < a.max_pages ? __ldcg(row + p) : -1;
-                some = some || e[k] != -1;
             }
-            if (!__syncthreads_or(some)) continue;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool held = (unsigned)e[k] < P;
-                const unsigned who = __ballot_sync(0xffffffffu, held);
-                if (lane == 0) s_held[warp] = __popc(who);
-                __syncthreads();
-                const int c = s_held[lane];
-                const int before_me = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
-                const long long to = at + before_me + __popc(who & ((1u << lane) - 1u));
-                if (held && to < a.P) a.free_list[to] = e[k];
-                if (e[k] != -1) row[p0 + k * NT + (int)threadIdx.x] = -1;
-                at += __reduce_add_sync(0xffffffffu, c);
-                __syncthreads();
+                who[k] = __ballot_sync(0xffffffffu, (unsigned)e[k] < P);
+                if (lane == 0) s_held[k][warp] = __popc(who[k]);
             }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = s_held[k][lane];
+                const int all = __reduce_add_sync(0xffffffffu, c);
+                if (all > 0) {
+                    const long long to = at + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(who[k] & ((1u << lane) - 1u));
+                    if ((unsigned)e[k] < P && to < a.P) a.free_list[to] = e[k];
+                }
+                if (e[k] != -1) row[p0 + k * NT + (int)threadIdx.x] = -1;
+                at += all;
+            }
+            __syncthreads();
         }
     }
     for (int i = threadIdx.x; i < mine; i += NT) a.first[n0 + i] = s_range[i].first;
@@ -341,21 +343,30 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
                 if (s_cu[mid] <= i0) lo = mid;
                 else hi = mid - 1;
             }
-            int n = lo, seen_n = -1, seen_p = -1;
+            // one division per four tokens: the others step through the pages
+            int n = lo, left = s_cu[n + 1] - i0, p = 0, off = 0;
             int32_t e = -1;
+            bool go = true;  // (n, p) is new: its table entry is not loaded yet
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u;
-                if (i >= total) break;
-                while (s_cu[n + 1] <= i) ++n;  // past sequences without tokens too
-                const unsigned pos = (unsigned)s_ctx[n] + (unsigned)(i - s_cu[n]);
-                const int p = (int)(pos / (unsigned)a.page);
-                if (n != seen_n || p != seen_p) {
-                    e = __ldcg(a.table + (int64_t)n * a.max_pages + p);
-                    seen_n = n;
-                    seen_p = p;
+                if (i0 + u >= total) break;
+                if (u == 0 || left == 0) {
+                    while (s_cu[n + 1] <= i0 + u) ++n;  // past sequences without tokens too
+                    const unsigned pos = (unsigned)s_ctx[n] + (unsigned)(i0 + u - s_cu[n]);
+                    p = (int)(pos / (unsigned)a.page);
+                    off = (int)(pos - (unsigned)p * (unsigned)a.page);
+                    left = s_cu[n + 1] - (i0 + u);
+                    go = true;
+                } else if (off == a.page) {
+                    ++p;
+                    off = 0;
+                    go = true;
                 }
-                if ((unsigned)e < P) out[u] = e * a.page + (int)(pos - (unsigned)p * (unsigned)a.page);
+                if (go) e = __ldcg(a.table + (int64_t)n * a.max_pages + p);
+                go = false;
+                if ((unsigned)e < P) out[u] = e * a.page + off;
+                ++off;
+                --left;
             }
         }
         if (i0 + 4 <= a.M) {
@@ -372,16 +383,24 @@ cudaError_t swska_page_tables_launch(const int64_t* ctx, const int32_t* n_new, i
                                      int32_t* free_list, int32_t* free_count, int32_t* cu, int32_t* slot, int N,
                                      int max_pages, int P, int page, int W, int S, int M, cudaStream_t stream) {
     const TableArgs a{ctx, n_new, table, first, free_list, free_count, cu, slot, N, max_pages, P, page, W, S, M};
-    // one CTA has a warp for each of 32 sequences and writes 4096 slots in one sweep; more work
-    // than that takes the largest portable cluster
-    const int CL = N <= NW && M <= 4 * NT ? 1 : kClusterMax;
+    // A CTA has a warp for each of 32 sequences and writes 4096 slots in one sweep. Clusters of 1, 8 and
+    // 16: the smallest that does all in one go, else 16 (256 decode sequences: 19.6 us with 8 CTAs, 22.3
+    // with 16, whose barriers take longer; 512 sequences with 180,000 new tokens: 39 and 33 us)
+    const int CL = N <= NW && M <= 4 * NT ? 1 : (N <= 8 * NW && M <= 8 * 4 * NT ? 8 : kClusterMax);
     const int per = (N + CL - 1) / CL;
     const size_t smem = ((size_t)10 * per + 2 * (size_t)N + 1) * sizeof(int32_t);
     static std::atomic<uint64_t> smem_set{0};
-    constexpr int kMost = (10 * (kMaxTableSeqs / kClusterMax) + 2 * kMaxTableSeqs + 1) * (int)sizeof(int32_t);
+    constexpr int kMost = (10 * (kMaxTableSeqs / kClusterMax) + 2 * kMaxTableSeqs + 1) * (int)sizeof(int32_t);  // CL = 16 there
     static_assert(kMost <= 220 * 1024, "shared memory");
     cudaError_t e = allow_smem(smem_set, (const void*)page_tables_kernel, kMost);
     if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> cluster_set{0};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= 64 || !(cluster_set.load(std::memory_order_relaxed) >> dev & 1)) {
+        if ((e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+        if (dev < 64) cluster_set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL);
     cfg.blockDim = dim3(NT);

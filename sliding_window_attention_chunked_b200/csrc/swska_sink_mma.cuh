@@ -9,9 +9,11 @@
 // different banks for every head dim. The kernels are bound by the latency of a tile's chain (copy, score
 // product, exponentials, second product): several CTAs an SM overlap theirs. A tcgen05 tile of 128 x 128
 // would leave most of itself empty at these sizes.
-// Probabilities and dS go to the second products in bf16 (relative 2^-9 each, as the inputs). D is not
-// taken from the rounded output: dq sums p dP of its rows in fp32 in a first sweep over the tiles, since
-// dS = p (dP - D) is a small difference where a row's attention is peaked.
+// Probabilities and dS go to the second products in bf16 (relative 2^-9 each, as the inputs). dS = p (dP -
+// D) is a small difference where a row's attention is peaked, and D from the rounded o is off by about
+// 2^-9 of it. So, as in swska_backward_tc.cu, dq sums e = sum p (dP - D) of its rows in fp32 on the
+// way, visits the first tile (where attention with first tokens peaks) last, with D + e, and sweeps
+// again where some p of another tile is above 1/2; the key side gets D + e.
 #pragma once
 
 #include <math.h>
@@ -251,10 +253,10 @@ sink_mma_fwd_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, 
 template <int DK, int DV> constexpr int dq_smem() { return 3 * (tile_bytes<DK>() + tile_bytes<DV>()); }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(NTH)
+__global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
-                   const float* __restrict__ lse, const bf16_t* __restrict__ dO, bf16_t* __restrict__ dq,
-                   float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
+                   const bf16_t* __restrict__ o, const float* __restrict__ lse, const bf16_t* __restrict__ dO,
+                   bf16_t* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
     const uint32_t sQ = smem_u32(sm), sG = sQ + tile_bytes<DK>(), stage = sQ + STAGE;
@@ -267,55 +269,87 @@ sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, c
     const KeyTiles kt = key_tiles(t0, T, W, S);
     copy_tile<DK>(sQ, q + bh * T * DK, t0, T);
     copy_tile<DV>(sG, dO + bh * T * DV, t0, T);
-    // two sweeps over the tiles: D, then dq
+    auto key0_of = [&](int i) { return kt.key0(i + 1 < kt.n ? i + 1 : 0); };  // the first tile last
     auto fetch = [&](int i) {
-        if (i < 2 * kt.n) {
-            const int key0 = kt.key0(i < kt.n ? i : i - kt.n);
-            copy_tile<DK>(stage + (i & 1) * STAGE, kb, key0, T);
-            copy_tile<DV>(stage + (i & 1) * STAGE + tile_bytes<DK>(), vb, key0, T);
+        if (i < kt.n) {
+            copy_tile<DK>(stage + (i & 1) * STAGE, kb, key0_of(i), T);
+            copy_tile<DV>(stage + (i & 1) * STAGE + tile_bytes<DK>(), vb, key0_of(i), T);
         }
         copies_done();
     };
     fetch(0);
     fetch(1);
-    float L2[2], D[2] = {0.f, 0.f}, acc[DK / 8][4];
+    float L2[2], D[2], e2[2] = {0.f, 0.f}, p_max = 0.f, acc[DK / 8][4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) L2[e] = t + 8 * e < T ? lse[bh * T + t + 8 * e] * kLog2e : INFINITY;  // past the end: p = 0
+    for (int e = 0; e < 2; ++e) {
+        const int row = t + 8 * e;
+        float d = 0.f;
+        if (row < T) {
+            const int64_t at = (bh * T + row) * DV + (DV / 4) * (lane % 4);  // a quarter of the row
+            if constexpr (DV >= 32) {
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+                for (int c = 0; c < DV / 4; c += 8) {
+                    float x[8], y[8];
+                    load8(o + at + c, x);
+                    load8(dO + at + c, y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-    for (int i = 0; i < 2 * kt.n; ++i) {
-        wait_but_one();
-        __syncthreads();
-        const uint32_t sK = stage + (i & 1) * STAGE, sV = sK + tile_bytes<DK>();
-        float s[8][4], g[8][4];
-        dot_tiles<DK>(sK, sQ, 16 * warp, s, lane);
-        mask_keys(s, t, t0, kt.key0(i < kt.n ? i : i - kt.n), W, S, c2);
-        dot_tiles<DV>(sV, sG, 16 * warp, g, lane);
-        if (i < kt.n) {
+                    for (int i = 0; i < 8; ++i) d = fmaf(x[i], y[i], d);
+                }
+            } else {
+                const float4 x = load4(o + at), y = load4(dO + at);
+                d = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+            }
+        }
+        D[e] = quad_sum(d);
+        L2[e] = row < T ? lse[bh * T + row] * kLog2e : INFINITY;  // past the end: p = 0
+    }
+    for (int sweep = 0; sweep < 2; ++sweep) {
+#pragma unroll
+        for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+        for (int i = 0; i < kt.n; ++i) {
+            wait_but_one();
+            __syncthreads();
+            const uint32_t sK = stage + (i & 1) * STAGE, sV = sK + tile_bytes<DK>();
+            float s[8][4], g[8][4];
+            dot_tiles<DK>(sK, sQ, 16 * warp, s, lane);
+            mask_keys(s, t, t0, key0_of(i), W, S, c2);
+            dot_tiles<DV>(sV, sG, 16 * warp, g, lane);
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    D[e / 2] = fmaf(tc::ex2(fmaf(s[n][e], scale_log2, -L2[e / 2])), g[n][e], D[e / 2]);
-            if (i == kt.n - 1) {
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] = tc::ex2(fmaf(s[n][e], scale_log2, -L2[e / 2]));
+                    if (sweep == 0) e2[e / 2] = fmaf(s[n][e], g[n][e] - D[e / 2], e2[e / 2]);
+                }
+            if (sweep == 0) {
+                if (i + 1 < kt.n) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    D[e] = quad_sum(D[e]);
-                    if (lane % 4 == 0 && t + 8 * e < T) dbuf[bh * T + t + 8 * e] = D[e];
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p_max = fmaxf(p_max, s[n][e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        D[e] += quad_sum(e2[e]);
+                        if (lane % 4 == 0 && t + 8 * e < T) dbuf[bh * T + t + 8 * e] = D[e];
+                    }
                 }
             }
-        } else {
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = tc::ex2(fmaf(s[n][e], scale_log2, -L2[e / 2])) * (g[n][e] - D[e / 2]);
+                for (int e = 0; e < 4; ++e) s[n][e] *= g[n][e] - D[e / 2];
             mul_tile<DK>(sK, s, acc, lane);
+            __syncthreads();
+            fetch(i + 2);
         }
-        __syncthreads();
-        fetch(i + 2);
+        if (sweep > 0 || !__syncthreads_or(p_max > 0.5f)) break;
+        fetch(0);
+        fetch(1);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     const float f[2] = {scale, scale};
     store_rows<DK / 8>(dq + bh * T * DK, t, T, DK, acc, f, c2);
 }
@@ -325,7 +359,7 @@ template <int DK, int DV> constexpr int dkv_smem() { return 3 * (tile_bytes<DK>(
 
 // blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
 template <int DK, int DV>
-__global__ void __launch_bounds__(NTH)
+__global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ dbuf, const bf16_t* __restrict__ dO,
                     bf16_t* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
@@ -446,7 +480,7 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     if ((e = allow_smem(k_set, (const void*)sink_mma_dkv_kernel<DK, DV>, kv_smem)) != cudaSuccess) return e;
     const bf16_t *q = static_cast<const bf16_t*>(a.q), *k = static_cast<const bf16_t*>(a.k), *v = static_cast<const bf16_t*>(a.v),
                  *dO = static_cast<const bf16_t*>(a.dO);
-    sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
+    sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
                                                                   a.W, a.S, a.scale, qtiles);
     sink_mma_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH, kv_smem, s>>>(
         q, k, v, a.lse, dbuf, dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
