@@ -47,8 +47,8 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = 2 * TILE_BYTES;
 constexpr int OFF_BAR = OFF_RING + NSLOT * TILE_BYTES;
-// full, empty, qfull, qempty, sfull[2], pfull[2], phalf[2], odone[2], meet[2], drain
-constexpr int NBAR = 2 * NSLOT + 13;
+// full, empty, qfull, qempty, sfull[2], pfull[2], phalf[2], odone[2], meet[2], drain, known[4]
+constexpr int NBAR = 2 * NSLOT + 17;
 constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
 constexpr int OFF_HAVE = OFF_MISC + 24;    // per key tile (mod 4): 8-row groups whose page exists
 constexpr int SMEM_BYTES = OFF_HAVE + 16 + 1024;
@@ -107,6 +107,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint64_t* odone = phalf + 2;
     uint64_t* meet = odone + 2;  // the softmax threads of a head, around the counter of a split tile
     uint64_t* drain = meet + 2;
+    uint64_t* known = drain + 1;  // [4]: `have` of a key tile is written
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
     volatile int* came_last = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);  // [2]
@@ -127,6 +128,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&meet[h], 128);
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&known[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -188,7 +190,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         break;
                     }
                     if (lane == 0) {
-                        if (which == 0) have[tiles & 3] = there;
+                        if (which == 0) {
+                            have[tiles & 3] = there;
+                            mbar_arrive(&known[tiles & 3]);
+                        }
                         mbar_arrive_expect_tx(&full[slot], TILE_BYTES);
                     }
                     __syncwarp();
@@ -325,10 +330,8 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tc::tmem_ld32(tS + 32, s + 32);
                 tc::tmem_ld32(tS + 64, s + 64);
                 tc::tmem_ld32(tS + 96, s + 96);
-                // the values' slot: held until this thread hands over P, so its phase cannot run ahead. Its
-                // barrier also covers `have`, written before it
-                const int Lv = Lb + 3 * j + 1 + h;
-                if (!wait_bar_warp(&full[Lv % NSLOT], (uint32_t)((Lv / NSLOT) & 1), abort_flag)) { ok = false; break; }
+                // written when the tile's keys were asked for, and not again before this head is done with it
+                if (!wait_bar_warp(&known[(tb + j) & 3], (uint32_t)(((tb + j) >> 2) & 1), abort_flag)) { ok = false; break; }
                 tc::tmem_wait_ld();
                 const int key0 = kt.at(u.kt0 + j) * BN;
                 const uint32_t there = have[(tb + j) & 3];
@@ -346,9 +349,16 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         for (int c = 0; c < 32; ++c)
                             if (!(v >> c & 1u)) s[32 * w + c] = 0xff800000u;
                     }
-                    // this thread's value row, if no query of the tile sees it
+                    // this thread's value row, if no query of the tile sees it: the slot is held until P is handed
+                    // over, so the phase of its barrier cannot run ahead
                     const int key = key0 + row;
                     const bool seen = (there >> (row / 8) & 1u) && key <= p1 && (key > p0 - a.W || key < a.S);
+                    const int Lv = Lb + 3 * j + 1 + h;
+                    if (!__all_sync(0xffffffffu, seen) &&
+                        !wait_bar_warp(&full[Lv % NSLOT], (uint32_t)((Lv / NSLOT) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
                     if (!seen) {
                         unsigned char* vr = smem + OFF_RING + (Lv % NSLOT) * TILE_BYTES + row * 128;
 #pragma unroll
