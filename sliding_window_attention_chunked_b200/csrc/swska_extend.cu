@@ -73,28 +73,28 @@ __device__ __forceinline__ SeqWork seq_work(const ExtendArgs& a, const ExtendPla
 __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, const ExtendPlan p) {
     // the attention kernel may set itself up meanwhile; it waits for this launch's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x > 0) {
-        // ---- new keys and values to their slots, 16 bytes a thread
-        if (a.k_new == nullptr) return;
-        const int ck = a.d_k * a.es / 16, cv = a.d_v * a.es / 16, per = ck + a.H * cv;
-        const int64_t n = (int64_t)a.M * per;
+    if (blockIdx.x >= 2) {
+        // ---- new keys and values to their slots, a warp per token
+        const int ck = a.d_k * a.es / 16, cv = a.d_v * a.es / 16, vl = __ffs(cv) - 1, per = ck + a.H * cv;  // 16-byte pieces
         const int64_t slots = (int64_t)a.P * a.page;
-        for (int64_t i = (int64_t)(blockIdx.x - 1) * NT + threadIdx.x; i < n; i += (int64_t)(gridDim.x - 1) * NT) {
-            const int row = (int)(i / per), c = (int)(i - (int64_t)row * per);
+        const int lane = threadIdx.x % 32;
+        for (int row = (int)(blockIdx.x - 2) * NW + (int)threadIdx.x / 32; row < a.M; row += (int)(gridDim.x - 2) * NW) {
             const int64_t slot = a.slot[row];
             if (slot < 0 || slot >= slots) continue;
-            const int64_t pg = slot / a.page;
-            const int off = (int)(slot - pg * a.page);
-            if (c < ck) {
-                static_cast<uint4*>(a.k_pool)[slot * ck + c] = static_cast<const uint4*>(a.k_new)[(int64_t)row * ck + c];
-            } else {
-                const int h = (c - ck) / cv, cc = (c - ck) % cv;
-                static_cast<uint4*>(a.v_pool)[((pg * a.H + h) * a.page + off) * cv + cc] =
-                    static_cast<const uint4*>(a.v_new)[((int64_t)row * a.H + h) * cv + cc];
+            const int pg = (int)slot / a.page, off = (int)slot - pg * a.page;
+            const uint4* kn = static_cast<const uint4*>(a.k_new) + (int64_t)row * ck;
+            const uint4* vn = static_cast<const uint4*>(a.v_new) + (int64_t)row * a.H * cv;
+            uint4* kp = static_cast<uint4*>(a.k_pool) + slot * ck;
+            uint4* vp = static_cast<uint4*>(a.v_pool) + ((int64_t)pg * a.H * a.page + off) * cv;
+#pragma unroll 4
+            for (int c = lane; c < per; c += 32) {
+                if (c < ck) kp[c] = kn[c];
+                else vp[(int64_t)((c - ck) >> vl) * a.page * cv + ((c - ck) & (cv - 1))] = vn[c - ck];
             }
         }
         return;
     }
+    if (blockIdx.x == 1 && p.r[1].rows == 0) return;
     __shared__ ExtendSeq s_seq[NT];  // the block of sequences at hand
     __shared__ Pair s_sums[NW];
     __shared__ int s_at[NT];         // first unit of each
@@ -102,13 +102,13 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
     __shared__ unsigned s_v[NT];     // first key tile in the line
     __shared__ unsigned s_most;
     __shared__ unsigned s_tiles[NT]; // key tiles in the line of each of its query tiles
-    // ---- rows of sequences at impossible positions
+    // ---- rows of sequences at impossible positions (block 0); s_seq for both
     for (int base = 0; base < a.N; base += NT) {
         const int n = base + (int)threadIdx.x;
         ExtendSeq mine{0, 0, 0, false};
         if (n < a.N) mine = extend_seq(a, n);
         s_seq[threadIdx.x] = mine;
-        if (!__syncthreads_or(mine.bad)) continue;
+        if (!__syncthreads_or(mine.bad) || blockIdx.x > 0) continue;
         for (int m = 0; m < NT; ++m) {
             const ExtendSeq s = s_seq[m];
             if (!s.bad) continue;
@@ -120,11 +120,11 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
         }
         __syncthreads();
     }
-    // ---- the units of each route; s_seq has every sequence if they are one block
+    // ---- the units of route blockIdx.x; s_seq has every sequence if they are one block
     const bool one_block = a.N <= NT;
-    for (int i = 0; i < 2; ++i) {
+    {
+        const int i = blockIdx.x;
         const ExtendRoute& r = p.r[i];
-        if (r.rows == 0) continue;
         for (int x = threadIdx.x; x < r.cols * a.H; x += NT) r.count[x] = 0;
         // this thread's sequence of a block: its query tiles and what each takes of the line
         auto work_at = [&](int base, int shift, unsigned* t) {
@@ -279,7 +279,7 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         route(0, kFewRows, few, kFewTile, (H + heads - 1) / heads, sms, 4, 6, N);
         p.short_len = kFewRows;
         if (max_len > kFewRows)
-            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 6, (int64_t)M / kChunkRows + N);
+            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 3, (int64_t)M / kChunkRows + N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
@@ -317,9 +317,8 @@ size_t swska_extend_workspace_size(int M, int N, int H, int dk, int dv, int max_
 cudaError_t swska_extend_launch(const ExtendArgs& a, bool bf16, cudaStream_t s) {
     ExtendPlan p = extend_plan(a.M, a.N, a.H, a.d_k, a.d_v, a.max_len, bf16);
     extend_bind(p, a.H, a.d_v, a.workspace);
-    const int64_t chunks = a.k_new ? (int64_t)a.M * (a.d_k + a.H * a.d_v) * a.es / 16 : 0;
-    const int64_t want = (chunks + NT - 1) / NT, cap = 8 * (int64_t)device_sm_count();
-    extend_prepare_kernel<<<1 + (unsigned)(want < cap ? want : cap), NT, 0, s>>>(a, p);
+    const int want = a.k_new ? (a.M + NW - 1) / NW : 0, cap = 8 * device_sm_count();
+    extend_prepare_kernel<<<2 + (unsigned)(want < cap ? want : cap), NT, 0, s>>>(a, p);
     note_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

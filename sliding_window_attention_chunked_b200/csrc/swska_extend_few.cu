@@ -12,7 +12,8 @@
 // memory with the 128-byte swizzle, which keeps the fragment loads free of bank conflicts; a page of
 // any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows. A warp issues a copy every 100
 // clocks or so, and a tile has to come every 3100 at HBM's rate, so a box takes the rows of all of
-// the CTA's heads: 4 copies a tile for pages of 32 k tokens, 16 for pages of 8 (18 and 72 head by head).
+// the CTA's heads, and two warps share them (one for the first 64 columns, one for the last): 4 copies a
+// tile for pages of 32 k tokens, 16 for pages of 8 (18 and 72 head by head).
 // Softmax: running maximum and sum in fp32, base 2; the output is rescaled only when a row's maximum
 // moves. Probabilities go to the second product in bf16 (relative 2^-9 each, like the cached values).
 #include <cuda.h>
@@ -37,7 +38,7 @@ constexpr int HD = 128;
 constexpr int KT = kFewTile;               // keys per tile
 constexpr int HALF = KT * 128;             // bytes: KT rows x 64 columns
 constexpr int TILE = 2 * HALF;             // 8 KB: a key tile or one head's value tile
-constexpr int NTH = 32 * (kFewHeads + 1);
+constexpr int NTH = 32 * (kFewHeads + 2);  // and two producer warps
 constexpr int MAXST = 12;
 constexpr int kMaxParts = 8;               // parts of a query tile, in units of 32 (see cols below)
 constexpr int RING = 216 * 1024;
@@ -87,9 +88,13 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // a CTA keeps to one head group: blockIdx.x = group + groups * column
     const int grp = blockIdx.x % r.groups;
     const int h0 = grp * hpg, nh = min(hpg, a.H - h0);
+    if (threadIdx.x == 32 * kFewHeads) {
+        tc::tma_prefetch_desc(&tm_k);
+        tc::tma_prefetch_desc(&tm_v);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);
             mbar_init(&empty[s], (uint32_t)nh);
         }
         *abort_flag = 0;
@@ -101,13 +106,10 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const ExtendRange range = load_range(r, blockIdx.x / r.groups);
 
-    if (warp == kFewHeads) {
-        // ------------------------------- producer -------------------------------
-        if (lane == 0) {
-            tc::tma_prefetch_desc(&tm_k);
-            tc::tma_prefetch_desc(&tm_v);
-        }
-        const int nbox = KT / box, ops = 4 * nbox;  // (keys, values) x halves x boxes: at most 16
+    if (warp >= kFewHeads) {
+        // ------------------------------- producers: one per half -------------------------------
+        const int half = warp - kFewHeads;
+        const int nbox = KT / box, ops = 2 * nbox;  // (keys, values) x boxes: at most 8
         int t = 0;  // tiles fed so far
         bool ok = true;
         for (int x = range.lo; x <= range.hi && ok; ++x) {
@@ -128,17 +130,17 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int b = 0; b < nbox; ++b)
                     if (__shfl_sync(0xffffffffu, pg, b) >= 0) have |= (box == 32 ? 0xffffffffu : ((1u << box) - 1u) << (b * box));
                 if (lane == 0) {
-                    mask[s] = have;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
+                    if (half == 0) mask[s] = have;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes / 2);
                 }
                 __syncwarp();
-                const int b = lane % nbox, half = lane / nbox % 2;
+                const int b = lane % nbox;
                 const int p = __shfl_sync(0xffffffffu, pg, b);
                 if (lane < ops) {
                     unsigned char* dst = smem + s * stage_bytes;
                     const int y = (key0 + b * box) % a.page;
                     // a page that the table does not have: a coordinate past the end, which fills zeros
-                    if (lane < 2 * nbox)
+                    if (lane < nbox)
                         tc::tma_load_3d(dst + half * HALF + b * box * 128, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[s]);
                     else
                         tc::tma_load_3d(dst + TILE + (half * nbox + b) * hpg * box * 128, &tm_v, half * 64, y,

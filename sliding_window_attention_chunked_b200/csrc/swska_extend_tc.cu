@@ -7,12 +7,13 @@
 // exponentials from about 100 queries up, by HBM below. The division of the warps, of tensor memory
 // and the order of the products are those of the contiguous prefill (swska_prefill_tc.cu):
 //   warps 0-3 / 4-7  softmax of head 0 / 1 (thread = query row = TMEM lane)
-//   warp 8           TMA: Q of the unit, then K_j, V0_j, V1_j through a ring of four 32 KB slots
-//   warp 9           TMEM allocation and MMA issue;  warps 10-11 idle (registers)
+//   warp 8, 10, 11   TMA: Q of the unit and K_j; V0_j; V1_j, through a ring of four 32 KB slots
+//   warp 9           TMEM allocation and MMA issue
 //   TMEM: S0 | O0 | S1 | O1;  S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
 // What the pages add: a tile of 128 keys arrives as boxes of as many rows as divide both the page
-// and 128, each lane of the producer warp issuing its own (page 8: 32 boxes, one per lane), with the
-// next tile's pages looked up while this one's copies run. A page that the table does not have is
+// and 128, each lane of a producer warp issuing its own (page 8: 32 boxes, one per lane; a warp issues
+// one in about 100 clocks, hence three such warps), with the next tile's pages looked up while this
+// one's copies run. A page that the table does not have is
 // fetched as zeros and masked. Rows of a tile that no query sees may hold anything, NaN included, and
 // 0 x NaN would reach the output, so the softmax warps clear those value rows before they hand over P
 // (the keys need no clearing: their scores are replaced).
@@ -113,6 +114,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     volatile int* came_last = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);  // [2]
     volatile uint32_t* have = reinterpret_cast<volatile uint32_t*>(smem + OFF_HAVE);
 
+    if (threadIdx.x == 256) {
+        tc::tma_prefetch_desc(&tm_q);
+        tc::tma_prefetch_desc(&tm_k);
+        tc::tma_prefetch_desc(&tm_v);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(&full[s], 1);
@@ -149,15 +155,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const ExtendRange range = load_range(r, blockIdx.x / r.groups);
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
-    if (warp == 8) {
-        // ------------------------------- TMA producer (all lanes) -------------------------------
-        if (lane == 0) {
-            tc::tma_prefetch_desc(&tm_q);
-            tc::tma_prefetch_desc(&tm_k);
-            tc::tma_prefetch_desc(&tm_v);
-        }
+    if (warp == 8 || warp >= 10) {
+        // ------------------------------- TMA producers (all lanes): keys, values of head 0, of head 1
+        const int which = warp == 8 ? 0 : warp - 9;
         const int nbox = BN / box;  // boxes of a tile's half: 1 .. 16
-        int L = 0, nq = 0, tiles = 0;
+        int nq = 0, tiles = 0;      // ring position of this warp's load of tile t: 3 t + which
         bool ok = true;
         for (int x = range.lo; x <= range.hi && ok; ++x) {
             const ExtendUnit u = load_unit(r.units + x);
@@ -168,52 +170,56 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 return i < u.kt1 && lane < nbox ? extend_page(a, u.n, (kt.at(i) * BN + lane * box) / a.page) : -1;
             };
             int pg_next = page_of(u.kt0);
-            if (nq > 0 && !wait_bar_warp(qempty, (uint32_t)((nq - 1) & 1), abort_flag)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(qfull, 2 * TILE_BYTES);
-                for (int h = 0; h < 2; ++h)
-                    for (int half = 0; half < 2; ++half)
-                        tc::tma_load_3d(smem + OFF_Q + h * TILE_BYTES + half * HALF_BYTES, &tm_q, half * 64,
-                                        u.row0 + u.q0, head[h], qfull);
+            if (which == 0) {
+                if (nq > 0 && !wait_bar_warp(qempty, (uint32_t)((nq - 1) & 1), abort_flag)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(qfull, 2 * TILE_BYTES);
+                    for (int h = 0; h < 2; ++h)
+                        for (int half = 0; half < 2; ++half)
+                            tc::tma_load_3d(smem + OFF_Q + h * TILE_BYTES + half * HALF_BYTES, &tm_q, half * 64,
+                                            u.row0 + u.q0, head[h], qfull);
+                }
+                ++nq;
             }
-            ++nq;
-            for (int i = u.kt0; i < u.kt1 && ok; ++i, ++tiles) {
+            for (int i = u.kt0; i < u.kt1; ++i, ++tiles) {
                 const int pg = pg_next, key0 = kt.at(i) * BN;
                 pg_next = page_of(i + 1);
                 uint32_t there = 0;  // bit per 8 rows
-                for (int b = 0; b < nbox; ++b)
-                    if (__shfl_sync(0xffffffffu, pg, b) >= 0) there |= ((1u << (box / 8)) - 1u) << (b * (box / 8));
-                for (int which = 0; which < 3; ++which, ++L) {
-                    const int slot = L % NSLOT, use = L / NSLOT;
-                    if (use > 0 && !wait_bar_warp(&empty[slot], (uint32_t)((use - 1) & 1), abort_flag)) {
-                        ok = false;
-                        break;
+                if (which == 0) {
+                    for (int b = 0; b < nbox; ++b)
+                        if (__shfl_sync(0xffffffffu, pg, b) >= 0) there |= ((1u << (box / 8)) - 1u) << (b * (box / 8));
+                }
+                const int L = 3 * tiles + which, slot = L % NSLOT, use = L / NSLOT;
+                if (use > 0 && !wait_bar_warp(&empty[slot], (uint32_t)((use - 1) & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (which == 0) {
+                        have[tiles & 3] = there;
+                        mbar_arrive(&known[tiles & 3]);
                     }
-                    if (lane == 0) {
-                        if (which == 0) {
-                            have[tiles & 3] = there;
-                            mbar_arrive(&known[tiles & 3]);
-                        }
-                        mbar_arrive_expect_tx(&full[slot], TILE_BYTES);
-                    }
-                    __syncwarp();
-                    // lane = (half, box)
-                    const int b = lane % 16, half = lane / 16;
-                    const int p = __shfl_sync(0xffffffffu, pg, b);
-                    if (b < nbox) {
-                        unsigned char* dst = smem + OFF_RING + slot * TILE_BYTES + half * HALF_BYTES + b * box * 128;
-                        const int y = (key0 + b * box) % a.page;
-                        if (which == 0) tc::tma_load_3d(dst, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[slot]);
-                        else tc::tma_load_3d(dst, &tm_v, half * 64, y, p >= 0 ? p * a.H + head[which - 1] : a.P * a.H,
-                                             &full[slot]);
-                    }
+                    mbar_arrive_expect_tx(&full[slot], TILE_BYTES);
+                }
+                __syncwarp();
+                // lane = (half, box)
+                const int b = lane % 16, half = lane / 16;
+                const int p = __shfl_sync(0xffffffffu, pg, b);
+                if (b < nbox) {
+                    unsigned char* dst = smem + OFF_RING + slot * TILE_BYTES + half * HALF_BYTES + b * box * 128;
+                    const int y = (key0 + b * box) % a.page;
+                    if (which == 0) tc::tma_load_3d(dst, &tm_k, half * 64, y, p >= 0 ? p : a.P, &full[slot]);
+                    else tc::tma_load_3d(dst, &tm_v, half * 64, y, p >= 0 ? p * a.H + head[which - 1] : a.P * a.H, &full[slot]);
                 }
             }
         }
-        // every copy that was started has landed before the CTA can leave
+        // every copy that this warp started has landed before the CTA can leave: those whose slot no later
+        // load takes (the others were used by products that have completed)
         if (nq > 0) mbar_wait_bounded(qfull, (uint32_t)((nq - 1) & 1), kWaitLimit);
-        for (int Li = (L > NSLOT ? L - NSLOT : 0); Li < L; ++Li)
-            mbar_wait_bounded(&full[Li % NSLOT], (uint32_t)((Li / NSLOT) & 1), kWaitLimit);
+        for (int t = tiles > 2 ? tiles - 2 : 0; t < tiles; ++t) {
+            const int L = 3 * t + which;
+            if (L + NSLOT >= 3 * tiles) mbar_wait_bounded(&full[L % NSLOT], (uint32_t)((L / NSLOT) & 1), kWaitLimit);
+        }
     } else if (warp == 9) {
         // ------------------------------- MMA issue (whole warp) -------------------------------
         const uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, 0, 0);
