@@ -364,9 +364,9 @@ ROD_API int rod_swska_cache_fill_fp8(const void* k, const void* v, void* k_cache
  * outputs dq, dk, dv in the layouts and dtype of q, k, v; workspace of
  * rod_swska_sink_backward_workspace_size bytes (its content on entry is irrelevant). Every sum is
  * taken in a fixed order: the results do not depend on timing.
- * Two routes, chosen by dtype and shape: ROD_BF16 with dk = dv = 128 and T >= 128 runs on the tensor
- * cores (bf16 probabilities and dS, fp32 accumulators), every other case on CUDA cores with fp32
- * FMAs.
+ * Routes: ROD_BF16 with dk = dv = 128 and T >= 128 runs on tcgen05, other ROD_BF16 shapes on
+ * warp-level matrix instructions (both: bf16 probabilities and dS, fp32 sums), ROD_FP32 on CUDA cores
+ * with fp32 FMAs.
  * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE (window < 1, sinks or dims unsupported, H > 64), ROD_ERR_ALIGN,
  * ROD_ERR_DTYPE, ROD_ERR_WORKSPACE, ROD_ERR_CUDA. T = 0 or B*H = 0 is a no-op.
  */
@@ -395,8 +395,10 @@ ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v,
  *   rod_swska_decode_paged);
  *   block_table [N][max_pages] int32: physical pages; an entry outside [0, P) is no page;
  *   slot_map [M] int32: row i of k_new / v_new is first written to slot slot_map[i] (physical page *
- *   page_size + row in the page); a slot outside [0, P * page_size) is not written;
- *   cu_seqlens [N+1] int32, not decreasing, cu_seqlens[0] >= 0; ctx [N] int64: tokens cached before.
+ *   page_size + row in the page); a slot outside [0, P * page_size) is not written, and no two rows
+ *   have the same one. Sequences may share pages that this call does not write (a common prefix);
+ *   cu_seqlens [N+1] int32, not decreasing, cu_seqlens[0] >= 0 (values outside [0, M] are cut to it;
+ *   where they fall, rows may be left as they are); ctx [N] int64: tokens cached before.
  * k_new, v_new and slot_map may be NULL together: nothing is written, the cache has the tokens.
  * Then query i of sequence n, at position p = ctx[n] + i, attends over the keys j <= p with
  * j > p - window or j < sinks, read from the cache. Keys of pages that the table does not have are
@@ -405,12 +407,14 @@ ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v,
  * position past 2^31 - 1 gets NaN rows. A sequence may have no new token.
  *   max_len: at most this many new tokens per sequence (a bound that picks the kernels; 0: M); of a
  *   longer sequence only the first max_len rows are computed.
- * workspace: rod_swska_extend_paged_workspace_size bytes, content irrelevant on entry. Two calls that
+ * workspace: rod_swska_extend_paged_workspace_size bytes (of the device that is current at the call),
+ * content irrelevant on entry. Two calls that
  * may overlap (two streams, two graphs) need a workspace each.
  * page_size: a positive multiple of 8; P * page_size and max_pages * page_size at most 2^31 - 1;
  * 1 <= H <= 64; 0 <= sinks <= ROD_MAX_SINKS; N <= ROD_MAX_EXTEND_SEQS.
- * Routes: ROD_BF16 with dk = dv = 128 runs on the tensor cores, every other case on CUDA cores with
- * fp32 FMAs. The result does not depend on timing.
+ * Routes: ROD_BF16 with dk = dv = 128 runs on the tensor cores (sequences of at most 16 new tokens on
+ * warp-level matrix instructions, longer ones on tcgen05; bf16 probabilities, fp32 sums), every other
+ * case on CUDA cores with fp32 FMAs. The result does not depend on timing.
  * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE, ROD_ERR_ALIGN (ctx: 8 bytes; int32 arrays: 4), ROD_ERR_DTYPE,
  * ROD_ERR_WORKSPACE, ROD_ERR_CUDA. M = 0 or N = 0 is a no-op.
  */
@@ -444,7 +448,8 @@ ROD_API int rod_swska_extend_paged(const void* q, const void* k_new, const void*
  *   cu_seqlens [N+1] int32, out: running sum of the tokens served (ctx is read only: the caller adds
  *   them);  slot_map [max_tokens] int32, 16-byte aligned, out: the slot of each served token in that
  *   order, -1 past the last (or where the table has no page).
- * A sequence with ctx < 0 is left alone. The result is a fixed function of the inputs.
+ * A sequence with ctx < 0 is left alone. No two rows of the table may hold the same page: it would go
+ * back twice. The result is a fixed function of the inputs.
  * page_size >= 1; P >= 1; max_pages >= 1; 0 <= N <= ROD_MAX_TABLE_SEQS; max_tokens >= 0;
  * P * page_size and max_pages * page_size at most 2^31 - 1; window >= 1; sinks >= 0.
  * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE, ROD_ERR_ALIGN, ROD_ERR_CUDA.

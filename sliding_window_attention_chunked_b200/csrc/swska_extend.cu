@@ -152,6 +152,12 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
             }
             if (all.v < 0x7fffffff) break;
         }
+        // Rows of two sequences at once (cu_seqlens that falls) could make more query tiles than there is
+        // room for: then nothing is computed
+        if (all.items > r.cap_items) {
+            for (int c = threadIdx.x; c < r.cols; c += NT) reinterpret_cast<int2*>(r.range)[c] = make_int2(1, 0);
+            return;
+        }
         // Even chunks cost r.split_cost key tiles more (parts to write and add). Whole query tiles, dealt
         // out with the longest one's room for each, are taken where that is less.
         if (threadIdx.x == 0) s_most = 0;

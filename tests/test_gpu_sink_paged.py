@@ -217,6 +217,20 @@ def test_extend_bad_cumulative_lengths_stay_inside():
     assert o.shape == keep.shape and torch.isfinite(o.float()[:2]).all()
 
 
+def test_extend_overlapping_sequences_stay_inside():
+    """cu_seqlens that claims the same rows many times over asks for more query tiles than the workspace holds: nothing is
+    written out of place (the rows are left as they are), and the next call is right."""
+    b = ref.Batch("bf16", 2, 128, 128, 60, 4, 16, [100] * 9, [40] + [0] * 8, seed=6)
+    args = b.args(DEV)
+    cu = torch.tensor([0, 40] * 5, dtype=torch.int32, device=DEV)
+    o = b.o.to(DEV)
+    work = torch.zeros(rod.load_library().rod_swska_extend_paged_workspace_size(40, 9, 2, 128, 128, 40, 1) + 4096, dtype=torch.uint8, device=DEV)
+    rod.swska_extend_paged(args[0], None, None, args[3], args[4], args[5], None, cu, args[8], 60, sinks=4, o=o, workspace=work[:-4096])
+    rod.check()
+    assert int(work[-4096:].sum()) == 0
+    _check_run(b, _run(b), "after")
+
+
 def test_extend_reads_only_and_negative_zero_lengths():
     """Without new keys and values the cache is read as it is; a batch without tokens does nothing."""
     b = ref.Batch("bf16", 4, 128, 128, 100, 4, 32, [300, 20], [5, 30], seed=3)
