@@ -279,10 +279,13 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
     const int sms = device_sm_count();
     if (bf16 && dk == 128 && dv == 128) {
         const int few = max_len < kFewRows ? max_len : kFewRows;
-        // Few sequences: four heads a CTA put twice the SMs to work and halve what one SM adds up at the
-        // end; many: eight share a key tile and keep two warps on each scheduler
-        const int heads = (int64_t)N * ((H + kFewHeads - 1) / kFewHeads) >= sms ? kFewHeads : kFewHeads / 2;
-        route(0, kFewRows, few, kFewTile, (H + heads - 1) / heads, sms, 4, 6, N);
+        // Up to four heads a CTA, two CTAs an SM, or up to eight and one: eight fetch a key tile once for
+        // all, four put twice the CTAs to work on small batches and leave each less to add up. H 16, W 4096:
+        // 17.5 us for 2 sequences with eight, 16.9 with four; 59.5 both for 16; 177 and 183 for 64, 335 and
+        // 346 for 128
+        const int heads = (int64_t)N * ((H + kFewHeads - 1) / kFewHeads) >= 48 ? kFewHeads : kFewHeads / 2;
+        const int groups = (H + heads - 1) / heads, hpg = (H + groups - 1) / groups;
+        route(0, kFewRows, few, kFewTile, groups, (hpg <= kFewHeads / 2 ? 2 : 1) * sms, 2, 6, N);
         p.short_len = kFewRows;
         if (max_len > kFewRows)
             route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 3, (int64_t)M / kChunkRows + N);

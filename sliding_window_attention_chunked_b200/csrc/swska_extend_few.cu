@@ -6,9 +6,10 @@
 // kernel is bound by reading the cache (values: H times the keys) from HBM. A CTA takes units (one
 // sequence, some key tiles of 32) of up to eight heads, so that the shared key tile is fetched once
 // for them: one warp per head, which multiplies with m16n8k16 instructions (16 query rows; a
-// tcgen05 tile of 128 rows would be seven eighths padding), and one warp that feeds a ring of
-// stages of a key tile and eight value tiles by TMA, 72 KB a stage: three stages hold more than the
-// bytes in flight that HBM's rate times its latency asks of an SM. The pages' rows land in shared
+// tcgen05 tile of 128 rows would be seven eighths padding), and two warps that feed a ring of
+// stages by TMA. With eight heads a stage (a key tile and eight value tiles) is 72 KB and an SM holds
+// three; with up to four, two CTAs an SM hold two stages of 40 KB each. Both are more than the bytes in
+// flight that HBM's rate times its latency asks of an SM (128 sequences, H 16, W 4096: 335 us, 6.9 TB/s). The pages' rows land in shared
 // memory with the 128-byte swizzle, which keeps the fragment loads free of bank conflicts; a page of
 // any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows. A warp issues a copy every 100
 // clocks or so, and a tile has to come every 3100 at HBM's rate, so a box takes the rows of all of
@@ -40,13 +41,15 @@ constexpr int HALF = KT * 128;             // bytes: KT rows x 64 columns
 constexpr int TILE = 2 * HALF;             // 8 KB: a key tile or one head's value tile
 constexpr int NTH = 32 * (kFewHeads + 2);  // and two producer warps
 constexpr int MAXST = 12;
-constexpr int kMaxParts = 8;               // parts of a query tile, in units of 32 (see cols below)
-constexpr int RING = 216 * 1024;
-constexpr int OFF_BAR = RING;
-constexpr int OFF_MASK = OFF_BAR + 2 * MAXST * 8;
+constexpr int kMaxParts = 10;              // parts of a query tile, in units of 32 (see cols below)
+// The ring for one CTA an SM (up to eight heads) or two (up to four): barriers and masks come first
+constexpr int OFF_MASK = 2 * MAXST * 8;
 constexpr int OFF_MISC = OFF_MASK + MAXST * 4;
-constexpr int SMEM = OFF_MISC + 16 + 1024;
-static_assert(SMEM <= 232448, "shared memory");
+constexpr int OFF_RING = 1024;
+static_assert(OFF_MISC + 16 <= OFF_RING, "barriers");
+constexpr int ring_for(int ctas) { return ctas == 1 ? 216 * 1024 : 104 * 1024; }
+constexpr int smem_for(int ctas) { return OFF_RING + ring_for(ctas) + 1024; }
+static_assert(smem_for(1) <= 232448 && 2 * (smem_for(2) + 1024) <= 233472, "shared memory");
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     for (uint32_t i = 1;; ++i) {
@@ -79,16 +82,17 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + MAXST;
     volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + OFF_MASK);  // keys whose page exists
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC);
+    unsigned char* ring = smem + OFF_RING;
     const int stage_bytes = TILE * (1 + hpg);
 
     // a CTA keeps to one head group: blockIdx.x = group + groups * column
     const int grp = blockIdx.x % r.groups;
     const int h0 = grp * hpg, nh = min(hpg, a.H - h0);
-    if (threadIdx.x == 32 * kFewHeads) {
+    if (threadIdx.x == 32 * hpg) {
         tc::tma_prefetch_desc(&tm_k);
         tc::tma_prefetch_desc(&tm_v);
     }
@@ -106,9 +110,9 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const ExtendRange range = load_range(r, blockIdx.x / r.groups);
 
-    if (warp >= kFewHeads) {
+    if (warp >= hpg) {
         // ------------------------------- producers: one per half -------------------------------
-        const int half = warp - kFewHeads;
+        const int half = warp - hpg;
         const int nbox = KT / box, ops = 2 * nbox;  // (keys, values) x boxes: at most 8
         int t = 0;  // tiles fed so far
         bool ok = true;
@@ -137,7 +141,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const int b = lane % nbox;
                 const int p = __shfl_sync(0xffffffffu, pg, b);
                 if (lane < ops) {
-                    unsigned char* dst = smem + s * stage_bytes;
+                    unsigned char* dst = ring + s * stage_bytes;
                     const int y = (key0 + b * box) % a.page;
                     // a page that the table does not have: a coordinate past the end, which fills zeros
                     if (lane < nbox)
@@ -153,7 +157,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             mbar_wait_bounded(&full[i % n_stages], (uint32_t)((i / n_stages) & 1), kWaitLimit);
         return;
     }
-    if (warp >= nh) return;
+    if (warp >= nh) return;  // the last group may have fewer heads
     // ------------------------------- one warp per head -------------------------------
     const int h = h0 + warp;
     const int g = lane / 4, c2 = 2 * (lane % 4);  // this thread's rows g, g + 8 and its column pair
@@ -189,7 +193,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = u.kt0; i < u.kt1; ++i, ++t) {
             const int st = t % n_stages, key0 = kt.at(i) * KT;
             if (!wait_warp(&full[st], (uint32_t)((t / n_stages) & 1), abort_flag)) return;
-            const uint32_t kb = smem_u32(smem + st * stage_bytes), vb = kb + TILE;
+            const uint32_t kb = smem_u32(ring + st * stage_bytes), vb = kb + TILE;
             float s[4][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -214,7 +218,7 @@ extend_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const bool seen = (have >> lane & 1u) && j <= p1 && ((int64_t)j > (int64_t)p0 - a.W || j < a.S);
                 zeroed = !__all_sync(0xffffffffu, seen);
                 if (!seen) {  // lane = key; neighbouring lanes start at neighbouring chunks: no bank conflicts
-                    unsigned char* v = smem + st * stage_bytes + TILE + rows_at(lane / 8, warp, hpg, box) + (lane & 7) * 128;
+                    unsigned char* v = ring + st * stage_bytes + TILE + rows_at(lane / 8, warp, hpg, box) + (lane & 7) * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         *reinterpret_cast<uint4*>(v + ((c + lane) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -436,14 +440,15 @@ cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, c
     if ((e = make_tmap_bf16_3d_strided(&mv, a.v_pool, HD, (uint64_t)a.page, (uint64_t)a.P * a.H, HD * 2, (uint64_t)a.page * HD * 2,
                                        64, (uint32_t)box, (uint32_t)hpg)) != cudaSuccess)
         return e;
-    int stages = RING / (TILE * (1 + hpg));
+    const int ctas = hpg <= kFewHeads / 2 ? 2 : 1;
+    int stages = ring_for(ctas) / (TILE * (1 + hpg));
     if (stages > MAXST) stages = MAXST;
     static std::atomic<uint64_t> smem_set{0};
-    if ((e = allow_smem(smem_set, (const void*)extend_few_kernel, SMEM)) != cudaSuccess) return e;
+    if ((e = allow_smem(smem_set, (const void*)extend_few_kernel, smem_for(1))) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(r.cols * r.groups));  // one CTA per SM
-    cfg.blockDim = dim3(NTH);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.gridDim = dim3((unsigned)(r.cols * r.groups));
+    cfg.blockDim = dim3(32 * (hpg + 2));
+    cfg.dynamicSmemBytes = smem_for(ctas);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
