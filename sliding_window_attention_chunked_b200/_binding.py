@@ -559,9 +559,9 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
     dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=dt, device=q.device)
+        o = torch.empty_like(v)
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H, T), dtype=torch.float32)
     _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, (B, H, T, dv)), ("o", o, dt, (B, H, T, dv)),
             ("lse", lse, torch.float32, (B, H, T)))
     _raise_on("rod_swska_sink_prefill",
@@ -607,7 +607,7 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     N, max_pages = _sizes(block_table, "block_table", 2)
     dev, dt = _index(q, "q"), q.dtype
     if o is None:
-        o = torch.empty((M, H, dv), dtype=dt, device=q.device)
+        o = q.new_empty((M, H, dv))
     _expect(dev, ("q", q, dt, (M, H, dk)), ("k_pool", k_pool, dt, (P, page, dk)), ("v_pool", v_pool, dt, (P, H, page, dv)),
             ("block_table", block_table, torch.int32, (N, max_pages)), ("ctx", ctx, torch.int64, (N,)),
             ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,)), ("o", o, dt, (M, H, dv)))
@@ -649,9 +649,9 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     if M < 0:
         raise ValueError("max_tokens must not be negative")
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(N + 1, dtype=i32, device=ctx.device)
+        cu_seqlens = first.new_empty(N + 1)
     if slot_map is None:
-        slot_map = torch.empty(M, dtype=i32, device=ctx.device)
+        slot_map = first.new_empty(M)
     _expect(dev, ("ctx", ctx, torch.int64, (N,)), ("n_new", n_new, i32, (N,)),
             ("block_table", block_table, i32, (N, max_pages)), ("first", first, i32, (N,)),
             ("free_list", free_list, i32, (P,)), ("free_count", free_count, i32, (1,)),
