@@ -376,6 +376,7 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t tP = tmem + lane_base + 128u + 64u * w;
         const uint32_t tQ = tmem + lane_base + 256u + 64u * w;
         const int t = t0 + row;
+        if (SINK) asm volatile("griddepcontrol.wait;" ::: "memory");  // the row statistics
         const float nL = nlse2[(int64_t)bh * Tpad + t];  // -inf past the end: p = 0
         float Dr = dbuf[(int64_t)bh * Tpad + t];
         const float2 sl2 = make_float2(scale_log2, scale_log2), nl2 = make_float2(nL, nL);
@@ -588,10 +589,7 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_holder;
-    if (SINK) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the query-tile kernel's statistics
-    }
+    if (SINK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 8) {
@@ -625,6 +623,7 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                     &full[slot]);
                 }
                 const int64_t srow = (int64_t)bh * Tpad + (int64_t)qt * TILE;
+                if (SINK && u == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the query-tile kernel's D
                 bulk_g2s(st, nlse2 + srow, TILE * 4, &full[slot]);
                 bulk_g2s(st + TILE * 4, dbuf + srow, TILE * 4, &full[slot]);
             }
@@ -846,6 +845,10 @@ __global__ void __launch_bounds__(256)
 ska_rowstats_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
                     const float* __restrict__ lse, float* __restrict__ nlse2, float* __restrict__ dbuf, int T,
                     int Tpad, int64_t rows) {
+    // after the launches before; then the next launch may set itself up (both matter only where it is
+    // launched to overlap, see swska_sink_backward_tc_launch)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (r >= rows) return;
@@ -984,6 +987,8 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     float* nlse2 = sink_parts_bind(parts, a);
     float* dbuf = nlse2 + (size_t)B * H * Tpad;
     // launch 1: the row statistics from the forward's output and log-sum-exp
+    // Each launch may set itself up, and fetch its inputs, while the one before ends: all that it
+    // fetches early was there before launch 1, which waits for all earlier work before it lets launch 2 in.
     const int64_t rows = (int64_t)B * H * Tpad;
     ska_rowstats_kernel<<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(
         static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2, dbuf, T,
@@ -1000,19 +1005,23 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     if ((e = allow_smem(k_set, (const void*)ska_bwd_dkdv_kernel<true>, ka::SMEM)) != cudaSuccess) return e;
     const int nqt = (int)(Tpad / TILE);
     const float sl = a.scale * kLog2e;
-    ska_bwd_dq_kernel<true><<<dim3((unsigned)nqt, (unsigned)H, (unsigned)B), NTHREADS, qa::SMEM_SINK, stream>>>(
-        mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), nlse2, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B);
-    cfg.blockDim = dim3(NTHREADS_KEY);
-    cfg.dynamicSmemBytes = ka::SMEM;
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)nqt, (unsigned)H, (unsigned)B);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = qa::SMEM_SINK;
+    if ((e = cudaLaunchKernelEx(&cfg, ska_bwd_dq_kernel<true>, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq),
+                                static_cast<const float*>(nlse2), dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S)) !=
+        cudaSuccess)
+        return e;
+    cfg.gridDim = dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B);
+    cfg.blockDim = dim3(NTHREADS_KEY);
+    cfg.dynamicSmemBytes = ka::SMEM;
     const float *cl = nlse2, *cd = dbuf;
     e = cudaLaunchKernelEx(&cfg, ska_bwd_dkdv_kernel<true>, mq, mdo, mk, mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv),
                            parts.dk_part, B, T, (int)Tpad, H, H / G, W, sl, nqt, a.S, parts);
