@@ -150,6 +150,23 @@ int device_sm_count();
 // the caller's, one per kernel
 cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes);
 
+// A launch that may begin while the one before it on the stream ends (once all CTAs of that one have
+// allowed it); the kernel itself waits for that end before it reads what the other wrote.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // forward (out, lse_out) or backward (o, lse, dO -> dq, dk, dv): query t sees the keys j <= t with
 // j > t - W or j < S
 struct SinkArgs {

@@ -88,16 +88,8 @@ float* sink_parts_bind(SinkParts& p, const SinkArgs& a) {
 cudaError_t sink_parts_reduce(const SinkParts& p, const SinkArgs& a, bool bf16, cudaStream_t s) {
     const int64_t n = (int64_t)p.B * p.T * p.dk / 4 + (p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0);
     const int64_t want = (n + 255) / 256, cap = 8 * (int64_t)device_sm_count();
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(want < cap ? want : cap));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, sink_reduce_kernel, p, a.dk, a.dv, bf16, a.scale);
+    const cudaError_t e = launch_overlapped(sink_reduce_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s, p, a.dk,
+                                            a.dv, bf16, a.scale);
     note_launches(1);
     return e;
 }

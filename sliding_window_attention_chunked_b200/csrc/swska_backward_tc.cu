@@ -1005,26 +1005,14 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     if ((e = allow_smem(k_set, (const void*)ska_bwd_dkdv_kernel<true>, ka::SMEM)) != cudaSuccess) return e;
     const int nqt = (int)(Tpad / TILE);
     const float sl = a.scale * kLog2e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)nqt, (unsigned)H, (unsigned)B);
-    cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = qa::SMEM_SINK;
-    if ((e = cudaLaunchKernelEx(&cfg, ska_bwd_dq_kernel<true>, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq),
-                                static_cast<const float*>(nlse2), dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt, a.S)) !=
-        cudaSuccess)
-        return e;
-    cfg.gridDim = dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B);
-    cfg.blockDim = dim3(NTHREADS_KEY);
-    cfg.dynamicSmemBytes = ka::SMEM;
     const float *cl = nlse2, *cd = dbuf;
-    e = cudaLaunchKernelEx(&cfg, ska_bwd_dkdv_kernel<true>, mq, mdo, mk, mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv),
-                           parts.dk_part, B, T, (int)Tpad, H, H / G, W, sl, nqt, a.S, parts);
+    e = launch_overlapped(ska_bwd_dq_kernel<true>, dim3((unsigned)nqt, (unsigned)H, (unsigned)B), dim3(NTHREADS), (size_t)qa::SMEM_SINK,
+                          stream, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), cl, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt,
+                          a.S);
+    if (e != cudaSuccess) return e;
+    e = launch_overlapped(ska_bwd_dkdv_kernel<true>, dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B), dim3(NTHREADS_KEY),
+                          (size_t)ka::SMEM, stream, mq, mdo, mk, mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T,
+                          (int)Tpad, H, H / G, W, sl, nqt, a.S, parts);
     note_launches(3);
     if (e != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, true, stream);

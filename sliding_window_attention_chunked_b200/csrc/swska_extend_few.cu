@@ -445,17 +445,8 @@ cudaError_t swska_extend_few_launch(const ExtendArgs& a, const ExtendRoute& r, c
     if (stages > MAXST) stages = MAXST;
     static std::atomic<uint64_t> smem_set{0};
     if ((e = allow_smem(smem_set, (const void*)extend_few_kernel, smem_for(1))) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(r.cols * r.groups));
-    cfg.blockDim = dim3(32 * (hpg + 2));
-    cfg.dynamicSmemBytes = smem_for(ctas);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, extend_few_kernel, mk, mv, a, r, hpg, stages, box, a.scale * 1.4426950408889634f);
+    e = launch_overlapped(extend_few_kernel, dim3((unsigned)(r.cols * r.groups)), dim3(32 * (hpg + 2)), (size_t)smem_for(ctas), s, mk, mv,
+                          a, r, hpg, stages, box, a.scale * 1.4426950408889634f);
     note_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -552,17 +552,8 @@ cudaError_t swska_extend_tc_launch(const ExtendArgs& a, const ExtendRoute& r, cu
         return e;
     static std::atomic<uint64_t> smem_set{0};
     if ((e = allow_smem(smem_set, (const void*)extend_tc_kernel, SMEM_BYTES)) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(r.cols * r.groups));  // one CTA per SM
-    cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, extend_tc_kernel, mq, mk, mv, a, r, box, a.scale * 1.4426950408889634f);
+    e = launch_overlapped(extend_tc_kernel, dim3((unsigned)(r.cols * r.groups)), dim3(NTHREADS), (size_t)SMEM_BYTES, s, mq, mk, mv, a, r,
+                          box, a.scale * 1.4426950408889634f);
     note_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

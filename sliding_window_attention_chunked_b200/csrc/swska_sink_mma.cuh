@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                    const bf16_t* __restrict__ o, const float* __restrict__ lse, const bf16_t* __restrict__ dO,
                    bf16_t* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
     const uint32_t sQ = smem_u32(sm), sG = sQ + tile_bytes<DK>(), stage = sQ + STAGE;
@@ -387,6 +388,7 @@ sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, 
         }
         copies_done();
     };
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the query side's D
     fetch(w.q_lo);
     fetch(w.q_lo + 1);
     float ak[DK / 8][4], av[DV / 8][4];
@@ -482,10 +484,12 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
                  *dO = static_cast<const bf16_t*>(a.dO);
     sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
                                                                   a.W, a.S, a.scale, qtiles);
-    sink_mma_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH, kv_smem, s>>>(
-        q, k, v, a.lse, dbuf, dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
-    note_launches(2);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_overlapped(sink_mma_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH), kv_smem,
+                          s, q, k, v, a.lse, static_cast<const float*>(dbuf), dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T,
+                          a.W, a.S, a.scale);
+    note_launches(2);
+    if (e != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, true, s);
 }
 

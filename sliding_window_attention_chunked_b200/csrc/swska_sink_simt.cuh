@@ -177,6 +177,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
                const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ dO,
                float* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     constexpr int NG = Dq<DK, DV>::NG;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) float sm[];
     const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sQ = sm;
@@ -277,6 +278,7 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     const int key0 = w.tile * BQ;
     load_tile<DK, BQ, NTH * NG>(sK, k, false, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
     load_tile<DV, BQ, NTH * NG>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the query side's D
     __syncthreads();
     const float scale_log2 = scale * kLog2e;
     float ak[4][DK / 16], av[4][DV / 16];
@@ -382,10 +384,12 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     if ((e = allow_smem(k_set, (const void*)sink_dkv_kernel<DK, DV>, K::smem)) != cudaSuccess) return e;
     sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
         f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
-    sink_dkv_kernel<DK, DV><<<dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), NTH * K::NG, K::smem, s>>>(
-        f32(a.q), f32(a.k), f32(a.v), a.lse, dbuf, f32(a.dO), static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
-    note_launches(2);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_overlapped(sink_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH * K::NG),
+                          K::smem, s, f32(a.q), f32(a.k), f32(a.v), a.lse, static_cast<const float*>(dbuf), f32(a.dO),
+                          static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
+    note_launches(2);
+    if (e != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, false, s);
 }
 
