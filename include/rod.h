@@ -363,7 +363,8 @@ ROD_API int rod_swska_cache_fill_fp8(const void* k, const void* v, void* k_cache
  *   dk_j = scale sum_h sum_t dS_tj q_t;  dv_j = sum_t p_tj dO_t (per head);
  * outputs dq, dk, dv in the layouts and dtype of q, k, v; workspace of
  * rod_swska_sink_backward_workspace_size bytes (its content on entry is irrelevant). Every sum is
- * taken in a fixed order: the results do not depend on timing.
+ * taken in a fixed order: the results do not depend on timing. Outputs and workspace overlap no
+ * input and not one another.
  * Routes: ROD_BF16 with dk = dv = 128 and T >= 128 runs on tcgen05, other ROD_BF16 shapes on
  * warp-level matrix instructions (both: bf16 probabilities and dS, fp32 sums), ROD_FP32 on CUDA cores
  * with fp32 FMAs.
@@ -409,7 +410,8 @@ ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v,
  *   longer sequence only the first max_len rows are computed.
  * workspace: rod_swska_extend_paged_workspace_size bytes (of the device that is current at the call),
  * content irrelevant on entry. Two calls that
- * may overlap (two streams, two graphs) need a workspace each.
+ * may overlap (two streams, two graphs) need a workspace each. o and the workspace overlap no input,
+ * and k_new and v_new are no part of the pools.
  * page_size: a positive multiple of 8; P * page_size and max_pages * page_size at most 2^31 - 1;
  * 1 <= H <= 64; 0 <= sinks <= ROD_MAX_SINKS; N <= ROD_MAX_EXTEND_SEQS.
  * Routes: ROD_BF16 with dk = dv = 128 runs on the tensor cores (sequences of at most 16 new tokens on
@@ -450,6 +452,7 @@ ROD_API int rod_swska_extend_paged(const void* q, const void* k_new, const void*
  *   order, -1 past the last (or where the table has no page).
  * A sequence with ctx < 0 is left alone. No two rows of the table may hold the same page: it would go
  * back twice. The result is a fixed function of the inputs.
+ * No two arrays overlap.
  * page_size >= 1; P >= 1; max_pages >= 1; 0 <= N <= ROD_MAX_TABLE_SEQS; max_tokens >= 0;
  * P * page_size and max_pages * page_size at most 2^31 - 1; window >= 1; sinks >= 0.
  * Errors: ROD_ERR_NULL, ROD_ERR_SHAPE, ROD_ERR_ALIGN, ROD_ERR_CUDA.

@@ -287,8 +287,12 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         const int groups = (H + heads - 1) / heads, hpg = (H + groups - 1) / groups;
         route(0, kFewRows, few, kFewTile, groups, (hpg <= kFewHeads / 2 ? 2 : 1) * sms, 2, 6, N);
         p.short_len = kFewRows;
+        // A cut in a tile's keys costs the parts' way through memory, 128 rows of 128 columns of 32 bits a head
+        // each, so whole query tiles are dealt out unless even chunks save more than twelve key tiles a CTA.
+        // With three and with twelve: 33 sequences of mixed lengths 66.8 and 52.4 us, one of 512 tokens with
+        // W 1000 44.8 and 37.8, twelve of 250 with H 5 47.5 and 40.0; one chunk with W 4096 is cut either way
         if (max_len > kFewRows)
-            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 3, (int64_t)M / kChunkRows + N);
+            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 12, (int64_t)M / kChunkRows + N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64

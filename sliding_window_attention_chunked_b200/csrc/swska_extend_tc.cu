@@ -484,7 +484,9 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!wait_bar_warp(&meet[h], (uint32_t)(meets++ & 1), abort_flag)) { ok = false; break; }
             if (!came_last[h]) continue;
             __threadfence();
-            // every thread adds its row: the maximum and sum first, then 32 columns at a time
+            // every thread adds its row: the maximum and sum first, then 32 columns at a time with the loads of
+            // four parts in flight. One chunk of 64 tokens, H 16, W 4096: 42.2 us with two parts, 43.1 with 16
+            // columns of eight, 38.2 so; one of 512 tokens 61.0, 59.3 and 57.9
             if (row >= rows) continue;
             float M = -INFINITY, Lsum = 0.f;
 #pragma unroll 4
@@ -499,22 +501,28 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 float4 O[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                for (int s = 0; s < u.nsplit; ++s) {
-                    const int part = u.part_of(s);
-                    const float m = __ldcg(&r.part_ml[r.part_at(part, a.H, hd, row)].x);
-                    float4 x4[8];
+                for (int s0 = 0; s0 < u.nsplit; s0 += 4) {
+                    float4 x4[4][8];
+                    float w[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x4[i] = __ldcg(reinterpret_cast<const float4*>(part_col(part, hd, cb / 4 + i)));
-                    if (m == -INFINITY) continue;  // nothing seen there; an empty part holds no output
-                    const float w = tc::ex2(m - base) * iv;
+                    for (int e = 0; e < 4; ++e) {
+                        const int part = u.part_of(s0 + e < u.nsplit ? s0 + e : 0);
+                        const float m = s0 + e < u.nsplit ? __ldcg(&r.part_ml[r.part_at(part, a.H, hd, row)].x) : -INFINITY;
+                        const float4* x = reinterpret_cast<const float4*>(part_col(part, hd, cb / 4));
+                        w[e] = tc::ex2(m - base) * iv;
+                        // nothing seen there (an empty part holds no output): zeros
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        O[i].x = fmaf(x4[i].x, w, O[i].x);
-                        O[i].y = fmaf(x4[i].y, w, O[i].y);
-                        O[i].z = fmaf(x4[i].z, w, O[i].z);
-                        O[i].w = fmaf(x4[i].w, w, O[i].w);
+                        for (int i = 0; i < 8; ++i) x4[e][i] = m != -INFINITY ? __ldcg(x + i * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            O[i].x = fmaf(x4[e][i].x, w[e], O[i].x);
+                            O[i].y = fmaf(x4[e][i].y, w[e], O[i].y);
+                            O[i].z = fmaf(x4[e][i].z, w[e], O[i].z);
+                            O[i].w = fmaf(x4[e][i].w, w[e], O[i].w);
+                        }
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
