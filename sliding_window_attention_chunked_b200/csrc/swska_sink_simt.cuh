@@ -34,6 +34,24 @@ using namespace simt;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// ROWS rows of D floats that follow one another into rows of D + 4, by asynchronous 16-byte copies that are all
+// in flight at once; rows from n on are zeros. A commit ends a set of them
+template <int D, int ROWS, int NTH>
+__device__ __forceinline__ void copy_tile(float* s, const float* from, int n, int tid = threadIdx.x) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(s);
+    if (ROWS * (D / 4) < NTH && tid >= ROWS * (D / 4)) return;
+#pragma unroll
+    for (int e = 0; e < (ROWS * (D / 4) + NTH - 1) / NTH; ++e) {
+        const int i = tid + e * NTH, r = i / (D / 4);
+        if (ROWS * (D / 4) % NTH != 0 && i >= ROWS * (D / 4)) break;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * (i + r)), "l"(r < n ? from + 4 * i : from),
+                     "r"(r < n ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER> __device__ __forceinline__ void copies_here() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
+
 constexpr int BQ = 32;
 constexpr int NTH = 4 * BQ;  // threads of a group
 // groups that fit: `own` floats for all, `each` per group, 227 KB in all
@@ -55,6 +73,7 @@ template <int DK, int DV> struct Dq {
 template <int DK, int DV> struct Dkv {
     static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP + 2 * BK;
     static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
+    static_assert(2 * BK == NTH, "a thread of the group per log-sum-exp and D of a tile");
 };
 
 // a group's sums (rows 4 ty + i, N columns a thread) to and from its buffers
@@ -104,9 +123,22 @@ sink_fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     const int t0 = (qtiles - 1 - (int)(blockIdx.x % qtiles)) * BQ;
     const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
-    load_tile<DK, BQ, NTH * NG>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
-    __syncthreads();
     const KeyTiles kt = key_tiles(t0, t1, W, S);
+    auto send_k = [&](int it) {
+        const int key0 = it < kt.n ? kt.at(it) * BK : T;
+        if (key0 < T) copy_tile<DK, BK, NTH>(sK, k + (b * (int64_t)T + key0) * (int64_t)DK, T - key0, tid);
+        copies_sent();
+    };
+    auto send_v = [&](int it) {
+        const int key0 = it < kt.n ? kt.at(it) * BK : T;
+        if (key0 < T) copy_tile<DV, BK, NTH>(sV, v + (bh * T + key0) * (int64_t)DV, T - key0, tid);
+        copies_sent();
+    };
+    copy_tile<DK, BQ, NTH * NG>(sQ, q + (bh * T + t0) * (int64_t)DK, T - t0);
+    send_k(g);
+    send_v(g);
+    copies_here<1>();
+    __syncthreads();
     float m[4], l[4], acc[4][N];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -117,9 +149,7 @@ sink_fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     }
     for (int it = g; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
-        group_sync<NTH>(g);
-        load_tile<DK, BK, NTH>(sK, k, false, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        copies_here<1>();
         group_sync<NTH>(g);
         float s[4][4];
         tile_dot<DK>(sQ, sK, ty, tx, s);
@@ -130,8 +160,12 @@ sink_fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
                 s[i][j] = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S) ? s[i][j] * scale_log2 : -INFINITY;
         softmax_step<N>(s, m, l, acc);
         put_tile(sP, ty, tx, s);
+        copies_here<0>();
         group_sync<NTH>(g);
+        send_k(it + NG);
         tile_mul<DV>(sP, sV, ty, tx, acc);
+        group_sync<NTH>(g);
+        send_v(it + NG);
     }
     if (NG > 1) {
         __syncthreads();
@@ -191,35 +225,53 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
     const int tx = tid % 16, ty = tid / 16;
     const int t1 = (t0 + BQ < T ? t0 + BQ : T) - 1;
     const float scale_log2 = scale * kLog2e;
-    load_tile<DK, BQ, NTH * NG>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; });
-    load_tile<DV, BQ, NTH * NG>(sG, dO, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; });
+    const KeyTiles kt = key_tiles(t0, t1, W, S);
+    auto send_k = [&](int it) {
+        const int key0 = it < kt.n ? kt.at(it) * BK : T;
+        if (key0 < T) copy_tile<DK, BK, NTH>(sK, k + (b * (int64_t)T + key0) * (int64_t)DK, T - key0, tid);
+        copies_sent();
+    };
+    auto send_v = [&](int it) {
+        const int key0 = it < kt.n ? kt.at(it) * BK : T;
+        if (key0 < T) copy_tile<DV, BK, NTH>(sV, v + (bh * T + key0) * (int64_t)DV, T - key0, tid);
+        copies_sent();
+    };
+    copy_tile<DV, BQ, NTH * NG>(sG, dO + (bh * T + t0) * (int64_t)DV, T - t0);
+    copy_tile<DK, BQ, NTH * NG>(sQ, q + (bh * T + t0) * (int64_t)DK, T - t0);
+    send_v(g0);
+    send_k(g0);
+    float L2[4], D[4], acc[4][DK / 16], out[4][DV / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) {
+            const int t = t0 + 4 * ty + i;
+            out[i][c] = t < T ? o[(bh * T + t) * (int64_t)DV + tx + 16 * c] : 0.f;
+        }
+    copies_here<1>();
     __syncthreads();
-    float L2[4], D[4], acc[4][DK / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, t = t0 + r;
         float d = 0.f;
-        if (t < T)
-            for (int c = tx; c < DV; c += 16) {
-                const int64_t at = (bh * T + t) * (int64_t)DV + c;
-                d = fmaf(sG[r * ld<DV>() + c], o[at], d);
-            }
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) d = fmaf(sG[r * ld<DV>() + tx + 16 * c], out[i][c], d);
         D[i] = row_sum(d);
         L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
         if (g0 == 0 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c) acc[i][c] = 0.f;
     }
-    const KeyTiles kt = key_tiles(t0, t1, W, S);
     for (int it = g0; it < kt.n; it += NG) {
         const int key0 = kt.at(it) * BK;
-        group_sync<NTH>(g0);
-        load_tile<DK, BK, NTH>(sK, k, false, [&](int r) { return key0 + r < T ? (b * T + key0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; }, tid);
+        copies_here<1>();
         group_sync<NTH>(g0);
         float s[4][4], g[4][4];
-        tile_dot<DK>(sQ, sK, ty, tx, s);
         tile_dot<DV>(sG, sV, ty, tx, g);
+        copies_here<0>();
+        group_sync<NTH>(g0);
+        send_v(it + NG);
+        tile_dot<DK>(sQ, sK, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -230,6 +282,8 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
         put_tile(sP, ty, tx, s);
         group_sync<NTH>(g0);
         tile_mul<DK>(sP, sK, ty, tx, acc);
+        group_sync<NTH>(g0);
+        send_k(it + NG);
     }
     if (NG > 1) {
         __syncthreads();
@@ -276,9 +330,29 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     const int tx = tid % 16, ty = tid / 16;
     const SinkWork w = parts.work((int)blockIdx.x);
     const int key0 = w.tile * BQ;
-    load_tile<DK, BQ, NTH * NG>(sK, k, false, [&](int r) { return key0 + r < T ? (b * (int64_t)T + key0 + r) * DK : -1; });
-    load_tile<DV, BQ, NTH * NG>(sV, v, false, [&](int r) { return key0 + r < T ? (bh * T + key0 + r) * (int64_t)DV : -1; });
+    auto send_g = [&](int qt) {
+        const int t0 = qt * BK;
+        if (qt <= w.q_hi) copy_tile<DV, BK, NTH>(sG, dO + (bh * T + t0) * (int64_t)DV, T - t0, tid);
+        copies_sent();
+    };
+    auto send_q = [&](int qt) {
+        const int t0 = qt * BK;
+        if (qt <= w.q_hi) {
+            copy_tile<DK, BK, NTH>(sQ, q + (bh * T + t0) * (int64_t)DK, T - t0, tid);
+            const int x = tid % BK;  // half of the threads: log-sum-exp, the others: D (2 BK = NTH)
+            const float* from = (tid < BK ? lse : dbuf) + (t0 + x < T ? bh * T + t0 + x : 0);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared((tid < BK ? sL : sD) + x)),
+                         "l"(from), "r"(t0 + x < T ? 4 : 0)
+                         : "memory");
+        }
+        copies_sent();
+    };
+    copy_tile<DV, BQ, NTH * NG>(sV, v + (bh * T + key0) * (int64_t)DV, T - key0);
+    copy_tile<DK, BQ, NTH * NG>(sK, k + (b * (int64_t)T + key0) * (int64_t)DK, T - key0);
+    send_g(w.q_lo + g0);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the query side's D
+    send_q(w.q_lo + g0);
+    copies_here<1>();
     __syncthreads();
     const float scale_log2 = scale * kLog2e;
     float ak[4][DK / 16], av[4][DV / 16];
@@ -291,33 +365,32 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     }
     for (int qt = w.q_lo + g0; qt <= w.q_hi; qt += NG) {
         const int t0 = qt * BK;
-        group_sync<NTH>(g0);
-        load_tile<DK, BK, NTH>(sQ, q, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DK : -1; }, tid);
-        load_tile<DV, BK, NTH>(sG, dO, false, [&](int r) { return t0 + r < T ? (bh * T + t0 + r) * (int64_t)DV : -1; }, tid);
-        for (int r = tid; r < BK; r += NTH) {
-            sL[r] = t0 + r < T ? lse[bh * T + t0 + r] * kLog2e : INFINITY;
-            sD[r] = t0 + r < T ? dbuf[bh * T + t0 + r] : 0.f;
-        }
+        copies_here<1>();
         group_sync<NTH>(g0);
         float s[4][4], g[4][4];  // rows: keys, columns: queries
-        tile_dot<DK>(sK, sQ, ty, tx, s);
         tile_dot<DV>(sV, sG, ty, tx, g);
+        copies_here<0>();
+        group_sync<NTH>(g0);
+        tile_dot<DK>(sK, sQ, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = tx + 16 * j;
-                const bool see = ska_visible(t0 + c, key0 + 4 * ty + i, W, S);
-                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -sL[c])) : 0.f;
+                const bool see = t0 + c < T && ska_visible(t0 + c, key0 + 4 * ty + i, W, S);
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -kLog2e * sL[c])) : 0.f;
                 g[i][j] = s[i][j] * (g[i][j] - sD[c]);
             }
         put_tile(sP, ty, tx, s);
         group_sync<NTH>(g0);
         tile_mul<DV>(sP, sG, ty, tx, av);
         group_sync<NTH>(g0);
+        send_g(qt + NG);
         put_tile(sP, ty, tx, g);
         group_sync<NTH>(g0);
         tile_mul<DK>(sP, sQ, ty, tx, ak);
+        group_sync<NTH>(g0);
+        send_q(qt + NG);
     }
     if (NG > 1) {
         __syncthreads();
