@@ -990,10 +990,11 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     // Each launch may set itself up, and fetch its inputs, while the one before ends: all that it
     // fetches early was there before launch 1, which waits for all earlier work before it lets launch 2 in.
     const int64_t rows = (int64_t)B * H * Tpad;
-    cudaError_t e = launch_overlapped(ska_rowstats_kernel, dim3((unsigned)((rows * 32 + 255) / 256)), dim3(256), 0, stream,
-                                      static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2,
-                                      dbuf, T, (int)Tpad, rows);
-    if (e != cudaSuccess) return e;
+    ska_rowstats_kernel<<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2, dbuf, T,
+        (int)Tpad, rows);
+    cudaError_t e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     CUtensorMap mq, mdo, mk, mv;
     if ((e = make_tmap_bf16_3d(&mq, a.q, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;
     if ((e = make_tmap_bf16_3d(&mdo, a.dO, HD, (uint64_t)T, (uint64_t)B * H, 64, TILE)) != cudaSuccess) return e;

@@ -169,7 +169,6 @@ swska_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const __nv_bfloat16* __restrict__ dO,
                 float* __restrict__ lse, float* __restrict__ dbuf, int Tpad, float lse_mul, int S_arg) {
     const int S = SINK ? S_arg : 0;
-    if (SINK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a backward may queue up behind
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -177,7 +177,6 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(NTH)
 sink_mma_fwd_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                     bf16_t* __restrict__ o, float* __restrict__ lse, int H, int T, int W, int S, float scale_log2, int qtiles) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a backward may queue up behind
     extern __shared__ __align__(16) unsigned char sm[];
     const uint32_t sQ = smem_u32(sm), stage = sQ + tile_bytes<DK>();
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
@@ -258,9 +257,7 @@ __global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                    const bf16_t* __restrict__ o, const float* __restrict__ lse, const bf16_t* __restrict__ dO,
                    bf16_t* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
-    // after all earlier launches (it may itself have been let in early); then the key side may set itself up
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
     const uint32_t sQ = smem_u32(sm), sG = sQ + tile_bytes<DK>(), stage = sQ + STAGE;
@@ -485,10 +482,9 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     if ((e = allow_smem(k_set, (const void*)sink_mma_dkv_kernel<DK, DV>, kv_smem)) != cudaSuccess) return e;
     const bf16_t *q = static_cast<const bf16_t*>(a.q), *k = static_cast<const bf16_t*>(a.k), *v = static_cast<const bf16_t*>(a.v),
                  *dO = static_cast<const bf16_t*>(a.dO);
-    e = launch_overlapped(sink_mma_dq_kernel<DK, DV>, dim3((unsigned)grid), dim3(NTH), q_smem, s, q, k, v,
-                          static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale,
-                          qtiles);
-    if (e != cudaSuccess) return e;
+    sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
+                                                                  a.W, a.S, a.scale, qtiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_overlapped(sink_mma_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH), kv_smem,
                           s, q, k, v, a.lse, static_cast<const float*>(dbuf), dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T,
                           a.W, a.S, a.scale);

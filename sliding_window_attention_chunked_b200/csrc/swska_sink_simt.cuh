@@ -112,7 +112,6 @@ sink_fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
                 float* __restrict__ o, float* __restrict__ lse, int H, int T, int W, int S, float scale_log2,
                 int qtiles) {
     constexpr int NG = Fwd<DK, DV>::NG, N = DV / 16;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a backward may queue up behind
     extern __shared__ __align__(16) float sm[];
     const int g = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sQ = sm;
@@ -212,9 +211,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
                const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ dO,
                float* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
     constexpr int NG = Dq<DK, DV>::NG;
-    // after all earlier launches (it may itself have been let in early); then the key side may set itself up
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) float sm[];
     const int g0 = threadIdx.x / NTH, tid = threadIdx.x % NTH;
     float* sQ = sm;
@@ -458,9 +455,9 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     static std::atomic<uint64_t> q_set{0}, k_set{0};
     if ((e = allow_smem(q_set, (const void*)sink_dq_kernel<DK, DV>, Q::smem)) != cudaSuccess) return e;
     if ((e = allow_smem(k_set, (const void*)sink_dkv_kernel<DK, DV>, K::smem)) != cudaSuccess) return e;
-    e = launch_overlapped(sink_dq_kernel<DK, DV>, dim3((unsigned)grid), dim3(NTH * Q::NG), Q::smem, s, f32(a.q), f32(a.k), f32(a.v),
-                          f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
-    if (e != cudaSuccess) return e;
+    sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
+        f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_overlapped(sink_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH * K::NG),
                           K::smem, s, f32(a.q), f32(a.k), f32(a.v), a.lse, static_cast<const float*>(dbuf), f32(a.dO),
                           static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
