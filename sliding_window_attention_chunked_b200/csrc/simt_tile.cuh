@@ -54,7 +54,7 @@ __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty,
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
     for (int d = 0; d < D; d += 4) {
         float4 x[4], y[4];
 #pragma unroll

@@ -17,6 +17,19 @@ struct SinkWork {
     int tile, slot, q_lo, q_hi;  // key tile, slot, query tiles [q_lo, q_hi]
 };
 
+// The order in which one CTA per SM takes (tile, head) pairs: up to 16 heads side by side, then the next tile
+// of each, so that the long tiles of all these heads start first and the short ones (a sequence's ends) fill
+// the last round; 148 CTAs are then some nine neighbouring tiles of each head, which share what they read
+// through L2. Head by head instead, the last head's long tiles end alone: 201 key tiles' time in place of 188
+// by count at T 8192, W 4096, H 16; 967 us a step and 940 so, alternated (the power cap takes the rest back).
+struct SinkOrder {
+    int rank, head;  // the tile's place in its head's order; the head (of all sequences)
+    static __device__ __forceinline__ SinkOrder of(int x, int tiles, int heads) {
+        const int g = x / (16 * tiles), r = x - g * 16 * tiles, n = heads - 16 * g < 16 ? heads - 16 * g : 16;
+        return {r / n, 16 * g + r % n};
+    }
+};
+
 struct SinkParts {
     int ks = 0, qs = 0, nk = 0, nq = 0;        // rows of a key tile and of a query tile, and their numbers
     int n_tiles = 0, nseg = 0, seg_len = 0;    // key tiles with far queries, segments each, query tiles per segment
@@ -31,6 +44,11 @@ struct SinkParts {
         return last < nq - 1 ? (int)last : nq - 1;
     }
     __host__ __device__ int ctas() const { return nk + n_tiles * nseg; }
+    // the CTA of place `rank` when the segments come first, which are no longer than the longest tiles
+    __device__ __forceinline__ int far_first(int rank) const {
+        const int far = n_tiles * nseg;
+        return rank < far ? nk + rank : rank - far;
+    }
     __device__ __forceinline__ SinkWork work(int x) const {
         SinkWork w;
         if (x < nk) {

@@ -196,9 +196,14 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int qt = n_qtiles - 1 - (int)blockIdx.x;  // full-window tiles first
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int bh = b * H + h;
+    int qt = n_qtiles - 1 - (int)blockIdx.x;  // full-window tiles first
+    int bh = blockIdx.z * H + blockIdx.y;
+    if (SINK) {
+        const SinkOrder at = SinkOrder::of((int)blockIdx.x, n_qtiles, (int)(gridDim.x / n_qtiles));
+        qt = n_qtiles - 1 - at.rank;
+        bh = at.head;
+    }
+    const int b = bh / H;
     const int t0 = qt * TILE;
     const int kt_lo = (t0 - W + 1 > 0 ? t0 - W + 1 : 0) / TILE;
     const int S = SINK ? S_arg : 0;
@@ -526,13 +531,17 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int grp = blockIdx.y, b = blockIdx.z;
+    int grp = blockIdx.y, b = blockIdx.z;
     int kt = blockIdx.x, qt_lo = kt;  // queries t in [j, j + W - 1] see key j
     int qt_hi = SinkParts::near_hi(kt, TILE, TILE, n_qtiles, W);  // the last query tile that sees the tile
     int slot = 0;
     const int S = SINK ? S_arg : 0;
     if (SINK) {
-        const SinkWork wk = parts.work((int)blockIdx.x);
+        const int tiles = parts.ctas(), G = H / HG;
+        const SinkOrder at = SinkOrder::of((int)blockIdx.x, tiles, (int)(gridDim.x / tiles));
+        grp = at.head % G;
+        b = at.head / G;
+        const SinkWork wk = parts.work(parts.far_first(at.rank));
         kt = wk.tile;
         qt_lo = wk.q_lo;
         qt_hi = wk.q_hi;
@@ -981,9 +990,10 @@ cudaError_t swska_backward_tc_launch(const SkaBackwardArgs& a, cudaStream_t stre
 cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream) {
     const int B = a.B, H = a.H, T = a.T, W = a.W;
     const int64_t Tpad = swska_backward_tc_tpad(T);
-    if (B > 65535) return cudaErrorInvalidConfiguration;
     const int G = swska_backward_tc_groups(B, H, T);
     SinkParts parts = sink_parts_plan(a, TILE, TILE, G);
+    const int64_t q_ctas = Tpad / TILE * B * H, k_ctas = (int64_t)parts.ctas() * B * G;
+    if (q_ctas > 0x7fffffffLL || k_ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     float* nlse2 = sink_parts_bind(parts, a);
     float* dbuf = nlse2 + (size_t)B * H * Tpad;
     // launch 1: the row statistics from the forward's output and log-sum-exp
@@ -1006,13 +1016,13 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     const int nqt = (int)(Tpad / TILE);
     const float sl = a.scale * kLog2e;
     const float *cl = nlse2, *cd = dbuf;
-    e = launch_overlapped(ska_bwd_dq_kernel<true>, dim3((unsigned)nqt, (unsigned)H, (unsigned)B), dim3(NTHREADS), (size_t)qa::SMEM_SINK,
+    e = launch_overlapped(ska_bwd_dq_kernel<true>, dim3((unsigned)q_ctas), dim3(NTHREADS), (size_t)qa::SMEM_SINK,
                           stream, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), cl, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt,
                           a.S);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(ska_bwd_dkdv_kernel<true>, dim3((unsigned)parts.ctas(), (unsigned)G, (unsigned)B), dim3(NTHREADS_KEY),
-                          (size_t)ka::SMEM, stream, mq, mdo, mk, mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T,
-                          (int)Tpad, H, H / G, W, sl, nqt, a.S, parts);
+    e = launch_overlapped(ska_bwd_dkdv_kernel<true>, dim3((unsigned)k_ctas), dim3(NTHREADS_KEY), (size_t)ka::SMEM, stream, mq, mdo, mk,
+                          mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T, (int)Tpad, H, H / G, W, sl, nqt, a.S,
+                          parts);
     note_launches(3);
     if (e != cudaSuccess) return e;
     return sink_parts_reduce(parts, a, true, stream);
