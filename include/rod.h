@@ -402,9 +402,9 @@ ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v,
  *   where they fall, rows may be left as they are); ctx [N] int64: tokens cached before.
  * k_new, v_new and slot_map may be NULL together: nothing is written, the cache has the tokens.
  * Then query i of sequence n, at position p = ctx[n] + i, attends over the keys j <= p with
- * j > p - window or j < sinks, read from the cache. Keys of pages that the table does not have are
- * left out (as pages behind the window are, once given back); a row that sees no key is 0. Memory
- * of a page past its sequence's last token may hold anything. A sequence with ctx[n] < 0 or a
+ * j > p - window or j < sinks, read from the cache (scale as for rod_swska_prefill). Keys of pages
+ * that the table does not have are left out (as pages behind the window are, once given back); a row
+ * that sees no key is 0. Memory of a page past its sequence's last token may hold anything. A sequence with ctx[n] < 0 or a
  * position past 2^31 - 1 gets NaN rows. A sequence may have no new token.
  *   max_len: at most this many new tokens per sequence (a bound that picks the kernels; 0: M); of a
  *   longer sequence only the first max_len rows are computed.

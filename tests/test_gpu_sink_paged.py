@@ -53,6 +53,16 @@ def test_training_step(B, H, T, dk, dv, W, S, dtype):
     _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"{dtype} T{T} W{W} S{S}")
 
 
+@pytest.mark.parametrize("B,H,T,W,S", [(3, 11, 300, 100, 5), (1, 40, 260, 129, 128), (17, 1, 500, 64, 2), (2, 16, 129, 200, 0), (9, 7, 130, 1, 1)])
+def test_training_step_many_heads(B, H, T, W, S):
+    """More (sequence, head) pairs than the 16 that go side by side, and a last set that is not full."""
+    q, k, v = wl.swska_inputs(B, H, T, 128, 128, seed=T + H, dtype="bf16", device=DEV)
+    dO = torch.randn_like(v)
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"B{B} H{H} T{T}")
+
+
 @pytest.mark.parametrize("dtype,T,W,S", [("bf16", 5000, 300, 4), ("bf16", 4100, 4096, 128), ("fp32", 1700, 90, 100), ("bf16", 20000, 64, 2)])
 def test_training_step_long(dtype, T, W, S):
     """Many far segments of the first tokens, and a window that ends just before the sequence does."""
