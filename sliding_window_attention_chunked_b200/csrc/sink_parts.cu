@@ -23,8 +23,10 @@ sink_reduce_kernel(const SinkParts p, void* __restrict__ dk, void* __restrict__ 
             s.w += t.w;
         };
         if (i < n_dk) {
-            const int64_t row = 4 * i / p.dk;
-            const int c = (int)(4 * i - row * p.dk), b = (int)(row / p.T), key = (int)(row % p.T);
+            const int64_t row = (4 * i) >> (__ffs(p.dk) - 1);  // dk is a power of two
+            const int b = (int)(row >> 32 == 0 ? (uint32_t)row / (uint32_t)p.T : row / p.T);
+            const int c = (int)(4 * i & (p.dk - 1)), key = (int)(row - (int64_t)b * p.T);
+#pragma unroll 8
             for (int g = 0; g < p.G; ++g) add(p.dk_part + (int64_t)g * n_dk * 4 + 4 * i);
             if (p.nseg > 0 && key < p.R)
                 for (int sl = 1; sl <= p.nseg; ++sl)

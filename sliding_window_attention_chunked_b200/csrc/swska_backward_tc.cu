@@ -847,9 +847,10 @@ ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 }
 
 // ============================================================================================
-// Launch 1 when the forward's output and log-sum-exp were kept: one warp per (padded) row,
-// lane l holding channels 4l .. 4l + 3, D = dO . o in fp32 and nlse2 = -lse * log2(e); rows
+// Launch 1 when the forward's output and log-sum-exp were kept: one warp per four (padded) rows, all loads
+// first, lane l holding channels 4l .. 4l + 3, D = dO . o in fp32 and nlse2 = -lse * log2(e); rows
 // past T get -inf and 0, as the statistics pass gives them.
+constexpr int ROWS_A_WARP = 4;
 __global__ void __launch_bounds__(256)
 ska_rowstats_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
                     const float* __restrict__ lse, float* __restrict__ nlse2, float* __restrict__ dbuf, int T,
@@ -858,30 +859,33 @@ ska_rowstats_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __
     // launched to overlap, see swska_sink_backward_tc_launch)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t r = ROWS_A_WARP * (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
     if (r >= rows) return;
     const int64_t bh = r / Tpad;
-    const int t = (int)(r - bh * Tpad);
-    if (t >= T) {
-        if (lane == 0) {
-            nlse2[r] = -INFINITY;
-            dbuf[r] = 0.f;
-        }
-        return;
-    }
-    const int64_t off = (bh * T + t) * HD + 4 * lane;
-    const uint2 ow = *reinterpret_cast<const uint2*>(o + off);
-    const uint2 gw = *reinterpret_cast<const uint2*>(dO + off);
-    float d = bf16lo(ow.x) * bf16lo(gw.x);
-    d = fmaf(bf16hi(ow.x), bf16hi(gw.x), d);
-    d = fmaf(bf16lo(ow.y), bf16lo(gw.y), d);
-    d = fmaf(bf16hi(ow.y), bf16hi(gw.y), d);
+    const int t = (int)(r - bh * Tpad), left = T - t;  // Tpad is a multiple of ROWS_A_WARP
+    uint2 ow[ROWS_A_WARP], gw[ROWS_A_WARP];
+    const float l = lane < ROWS_A_WARP && lane < left ? lse[bh * T + t + lane] : 0.f;
 #pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) d += __shfl_xor_sync(0xffffffffu, d, sh);
-    if (lane == 0) {
-        dbuf[r] = d;
-        nlse2[r] = -lse[bh * T + t] * kLog2e;
+    for (int e = 0; e < ROWS_A_WARP; ++e) {
+        const int64_t off = (bh * T + t + e) * HD + 4 * lane;
+        ow[e] = e < left ? *reinterpret_cast<const uint2*>(o + off) : make_uint2(0, 0);
+        gw[e] = e < left ? *reinterpret_cast<const uint2*>(dO + off) : make_uint2(0, 0);
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int e = 0; e < ROWS_A_WARP; ++e) {
+        float d = bf16lo(ow[e].x) * bf16lo(gw[e].x);
+        d = fmaf(bf16hi(ow[e].x), bf16hi(gw[e].x), d);
+        d = fmaf(bf16lo(ow[e].y), bf16lo(gw[e].y), d);
+        d = fmaf(bf16hi(ow[e].y), bf16hi(gw[e].y), d);
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) d += __shfl_xor_sync(0xffffffffu, d, sh);
+        if (lane == e) mine = d;
+    }
+    if (lane < ROWS_A_WARP) {
+        dbuf[r + lane] = mine;
+        nlse2[r + lane] = lane < left ? -l * kLog2e : -INFINITY;
     }
 }
 
@@ -950,7 +954,7 @@ cudaError_t swska_backward_tc_launch(const SkaBackwardArgs& a, cudaStream_t stre
     cudaError_t e;
     if (a.o != nullptr && a.lse != nullptr) {
         const int64_t rows = (int64_t)B * H * Tpad;
-        ska_rowstats_kernel<<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(
+        ska_rowstats_kernel<<<(unsigned)((rows / ROWS_A_WARP * 32 + 255) / 256), 256, 0, stream>>>(
             static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2, dbuf,
             T, (int)Tpad, rows);
         note_launches(1);
@@ -1000,7 +1004,7 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     // Each launch may set itself up, and fetch its inputs, while the one before ends: all that it
     // fetches early was there before launch 1, which waits for all earlier work before it lets launch 2 in.
     const int64_t rows = (int64_t)B * H * Tpad;
-    ska_rowstats_kernel<<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(
+    ska_rowstats_kernel<<<(unsigned)((rows / ROWS_A_WARP * 32 + 255) / 256), 256, 0, stream>>>(
         static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dO), a.lse, nlse2, dbuf, T,
         (int)Tpad, rows);
     cudaError_t e;
