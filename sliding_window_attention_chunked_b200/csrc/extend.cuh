@@ -32,6 +32,7 @@ struct ExtendRoute {
     int groups = 1;          // head groups
     int cols = 1;            // CTAs per head group
     int min_chunk = 1;       // key tiles that a CTA takes at least
+    int rows_div = 0;        // > 0: a CTA takes at least sqrt(key tiles x rows of the largest query tile / rows_div)
     int split_cost = 0;      // what the parts of a cut query tile cost, in key tiles
     int part_rows = 0;       // rows kept of a part
     int cap_items = 0;

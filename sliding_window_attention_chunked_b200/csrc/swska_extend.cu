@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
     __shared__ int s_at[NT];         // first unit of each
     __shared__ int s_item[NT];       // first query tile
     __shared__ unsigned s_v[NT];     // first key tile in the line
-    __shared__ unsigned s_most;
+    __shared__ unsigned s_most, s_rows;  // the largest query tile: key tiles, and key tiles x rows
     __shared__ unsigned s_tiles[NT]; // key tiles in the line of each of its query tiles
     // ---- rows of sequences at impossible positions (block 0); s_seq for both
     for (int base = 0; base < a.N; base += NT) {
@@ -160,17 +160,29 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
         }
         // Even chunks cost r.split_cost key tiles more (parts to write and add). Whole query tiles, dealt
         // out with the longest one's room for each, are taken where that is less.
-        if (threadIdx.x == 0) s_most = 0;
+        if (threadIdx.x == 0) s_most = s_rows = 0;
         __syncthreads();
         for (int base = 0; base < a.N; base += NT) {
             if (!one_block) work_at(base, shift, &t);
-            if (t > 0) atomicMax(&s_most, t);
+            if (t > 0) {
+                atomicMax(&s_most, t);
+                const int len = s_seq[threadIdx.x].len;
+                atomicMax(&s_rows, t * (unsigned)(len < r.rows ? len : r.rows));
+            }
         }
         __syncthreads();
         const unsigned t_max = s_most;
         unsigned V = (unsigned)all.v;
         const unsigned even = (V + r.cols - 1) / r.cols, rounds = ((unsigned)all.items + r.cols - 1) / r.cols;
         unsigned Q = even > (unsigned)r.min_chunk ? even : r.min_chunk;
+        // Small batches: a part's rows are read back by the one that adds them, so n chunks of a tile of x key
+        // tiles take a CTA x / n tiles' time and then n parts' rows; n = sqrt(x / rows) is least for the two. (Chunks of
+        // at least two key tiles and so: one sequence of 16 tokens with W 4096 80.1 and 37.1 us, of 8 46.9 and 27.8, of
+        // 2 21.4 and 18.3; of 16 with W 500 22.9 and 18.9. Half and twice the divisor: within 10% of that.)
+        if (r.rows_div > 0) {
+            const unsigned q = (unsigned)ceilf(sqrtf((float)s_rows / (float)r.rows_div));
+            Q = q > Q ? q : Q;
+        }
         const bool whole = (unsigned long long)rounds * t_max <= (unsigned long long)Q + r.split_cost;
         if (whole) {
             Q = rounds * t_max;
@@ -264,7 +276,7 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
     ExtendPlan p;
     if (max_len > M) max_len = M;
     // ctas: what the GPU holds at once
-    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int split_cost,
+    auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int rows_div, int split_cost,
                      int64_t items) {
         ExtendRoute& r = p.r[i];
         r.rows = rows;
@@ -273,6 +285,7 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         r.groups = groups;
         r.cols = ctas / groups > 1 ? ctas / groups : 1;
         r.min_chunk = min_chunk;
+        r.rows_div = rows_div;
         r.split_cost = split_cost;
         r.cap_items = (int)(items < M ? items : M);
     };
@@ -285,19 +298,19 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         // 346 for 128
         const int heads = (int64_t)N * ((H + kFewHeads - 1) / kFewHeads) >= 48 ? kFewHeads : kFewHeads / 2;
         const int groups = (H + heads - 1) / heads, hpg = (H + groups - 1) / groups;
-        route(0, kFewRows, few, kFewTile, groups, (hpg <= kFewHeads / 2 ? 2 : 1) * sms, 2, 6, N);
+        route(0, kFewRows, few, kFewTile, groups, (hpg <= kFewHeads / 2 ? 2 : 1) * sms, 2, 16, 6, N);
         p.short_len = kFewRows;
         // A cut in a tile's keys costs the parts' way through memory, 128 rows of 128 columns of 32 bits a head
         // each, so whole query tiles are dealt out unless even chunks save more than twelve key tiles a CTA.
         // With three and with twelve: 33 sequences of mixed lengths 66.8 and 52.4 us, one of 512 tokens with
         // W 1000 44.8 and 37.8, twelve of 250 with H 5 47.5 and 40.0; one chunk with W 4096 is cut either way
         if (max_len > kFewRows)
-            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 12, (int64_t)M / kChunkRows + N);
+            route(1, kChunkRows, kChunkRows, kChunkTile, (H + 1) / 2, sms, 4, 0, 12, (int64_t)M / kChunkRows + N);
         return p;
     }
     // CUDA cores: 16 queries a tile while every sequence has few, else 64
     const int rows = max_len <= 16 ? 16 : 64;
-    route(0, rows, rows, 64, H, (rows == 16 ? 4 : 2) * sms, 1, 1, (int64_t)M / rows + N);
+    route(0, rows, rows, 64, H, (rows == 16 ? 4 : 2) * sms, 1, 0, 1, (int64_t)M / rows + N);
     return p;
 }
 
