@@ -164,10 +164,12 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
         __syncthreads();
         for (int base = 0; base < a.N; base += NT) {
             if (!one_block) work_at(base, shift, &t);
-            if (t > 0) {
-                atomicMax(&s_most, t);
-                const int len = s_seq[threadIdx.x].len;
-                atomicMax(&s_rows, t * (unsigned)(len < r.rows ? len : r.rows));
+            const int len = t > 0 ? s_seq[threadIdx.x].len : 0;
+            const unsigned most = __reduce_max_sync(0xffffffffu, t);
+            const unsigned rows = __reduce_max_sync(0xffffffffu, t * (unsigned)(len < r.rows ? len : r.rows));
+            if (threadIdx.x % 32 == 0 && most > 0) {
+                atomicMax(&s_most, most);
+                atomicMax(&s_rows, rows);
             }
         }
         __syncthreads();
