@@ -198,6 +198,17 @@ def test_extend(H, W, S, page, ctx, lens, pad, dtype, dk, dv):
         _check_run(b, _run(b), f"{dtype} {dk} H{H} W{W} no max_len")
 
 
+@pytest.mark.parametrize("lens", [[2], [3], [4], [5], [8], [9], [15], [16], [16, 1, 2], [7, 0, 13]])
+def test_extend_few_tokens_over_a_long_window(lens):
+    """Few rows over many keys: every tile is cut, and rows of two, four, eight and more are added together."""
+    b = ref.Batch("bf16", 5, 128, 128, 2500, 4, 64, [2600 + 900 * i for i in range(len(lens))], lens, pad=2, seed=sum(lens))
+    got = _run(b, max_len=b.max_len)
+    rod.check()
+    _check_run(b, got, f"few {lens}")
+    again = _run(b, max_len=16)[0]
+    assert torch.equal(_run(b, max_len=16)[0].view(torch.int16), again.view(torch.int16))  # no order depends on timing
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_extend_hostile_tables(dtype):
     """Entries and slots outside the pool, positions past the table, bad ctx, a bound below a length: nothing outside is
