@@ -179,6 +179,7 @@ struct SinkArgs {
     void *dq, *dk, *dv;
     int B, H, T, d_k, d_v, W, S;  // W clamped to T
     float scale;
+    float grad_scale;  // backward: of dq and dk; 0 where no row sees a second key (p = 1, so dS = 0)
     void* workspace;
 };
 cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t s);  // bf16, dk = dv = 128, T >= 128

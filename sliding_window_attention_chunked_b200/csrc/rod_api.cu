@@ -397,6 +397,7 @@ int rod_swska_sink_backward(const void* q, const void* k, const void* v, const v
     a.q = q, a.k = k, a.v = v, a.o = o, a.lse = lse, a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
     a.B = B, a.H = H, a.T = T, a.d_k = dk_dim, a.d_v = dv_dim, a.W = window < T ? window : T, a.S = sinks;
     a.scale = resolve_scale(scale, dk_dim);
+    a.grad_scale = T == 1 || (window == 1 && sinks == 0) ? 0.f : a.scale;
     a.workspace = workspace;
     return from_cuda(rod::swska_sink_backward_launch(a, dtype == ROD_BF16, static_cast<cudaStream_t>(stream)));
 }

@@ -91,7 +91,7 @@ cudaError_t sink_parts_reduce(const SinkParts& p, const SinkArgs& a, bool bf16, 
     const int64_t n = (int64_t)p.B * p.T * p.dk / 4 + (p.nseg > 0 ? (int64_t)p.B * p.H * p.R * p.dv / 4 : 0);
     const int64_t want = (n + 255) / 256, cap = 8 * (int64_t)device_sm_count();
     const cudaError_t e = launch_overlapped(sink_reduce_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s, p, a.dk,
-                                            a.dv, bf16, a.scale);
+                                            a.dv, bf16, a.grad_scale);
     note_launches(1);
     return e;
 }

@@ -79,7 +79,7 @@ SinkParts sink_parts_plan(const SinkArgs& a, int ks, int qs, int G);
 size_t sink_parts_floats(const SinkParts& p);
 // sets the pointers inside a.workspace; returns the statistics array (2 B H Tpad floats)
 float* sink_parts_bind(SinkParts& p, const SinkArgs& a);
-// dk = scale * (all parts), and dv of the first S keys where they have parts
+// dk = grad_scale * (all parts), and dv of the first S keys where they have parts
 cudaError_t sink_parts_reduce(const SinkParts& p, const SinkArgs& a, bool bf16, cudaStream_t s);
 
 }  // namespace rod

@@ -1021,8 +1021,8 @@ cudaError_t swska_sink_backward_tc_launch(const SinkArgs& a, cudaStream_t stream
     const float sl = a.scale * kLog2e;
     const float *cl = nlse2, *cd = dbuf;
     e = launch_overlapped(ska_bwd_dq_kernel<true>, dim3((unsigned)q_ctas), dim3(NTHREADS), (size_t)qa::SMEM_SINK,
-                          stream, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), cl, dbuf, T, (int)Tpad, H, W, sl, a.scale, nqt,
-                          a.S);
+                          stream, mq, mdo, mk, mv, static_cast<__nv_bfloat16*>(a.dq), cl, dbuf, T, (int)Tpad, H, W, sl, a.grad_scale,
+                          nqt, a.S);
     if (e != cudaSuccess) return e;
     e = launch_overlapped(ska_bwd_dkdv_kernel<true>, dim3((unsigned)k_ctas), dim3(NTHREADS_KEY), (size_t)ka::SMEM, stream, mq, mdo, mk,
                           mv, cl, cd, static_cast<__nv_bfloat16*>(a.dv), parts.dk_part, B, T, (int)Tpad, H, H / G, W, sl, nqt, a.S,

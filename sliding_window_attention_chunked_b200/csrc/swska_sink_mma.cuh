@@ -256,7 +256,8 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
                    const bf16_t* __restrict__ o, const float* __restrict__ lse, const bf16_t* __restrict__ dO,
-                   bf16_t* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
+                   bf16_t* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale,
+                   float grad_scale, int qtiles) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) unsigned char sm[];
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
@@ -351,7 +352,7 @@ sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, c
         fetch(1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const float f[2] = {scale, scale};
+    const float f[2] = {grad_scale, grad_scale};
     store_rows<DK / 8>(dq + bh * T * DK, t, T, DK, acc, f, c2);
 }
 
@@ -483,7 +484,7 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     const bf16_t *q = static_cast<const bf16_t*>(a.q), *k = static_cast<const bf16_t*>(a.k), *v = static_cast<const bf16_t*>(a.v),
                  *dO = static_cast<const bf16_t*>(a.dO);
     sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
-                                                                  a.W, a.S, a.scale, qtiles);
+                                                                  a.W, a.S, a.scale, a.grad_scale, qtiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_overlapped(sink_mma_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH), kv_smem,
                           s, q, k, v, a.lse, static_cast<const float*>(dbuf), dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T,

@@ -236,29 +236,44 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
         if (key0 < T) copy_tile<DV, BK, NTH>(sV, v + (bh * T + key0) * (int64_t)DV, T - key0, tid);
         copies_sent();
     };
+    // D = dO . o of a row, summed by one thread in tile_dot's order: where a row gives one key all of its
+    // attention, o is that key's v and dP - D is exactly 0, not the difference of two roundings (shared out over
+    // 16 threads a row, dq and dk of rows that see one key were 1e-7 |dO| |v| of noise). The rows of o wait in the dS
+    // tiles, 64 columns to a group's.
+    static_assert(DV <= BK || NG >= 2, "room for the rows of o");
+    float* sO = sm + Dq<DK, DV>::own + BK * (ld<DK>() + ld<DV>());
+    auto o_at = [&](int r, int c) { return sO + (c / BK) * Dq<DK, DV>::each + r * LDP + c % BK; };
+    for (int i = threadIdx.x; i < BQ * (DV / 4); i += NTH * NG) {
+        const int r = i / (DV / 4), c = 4 * (i % (DV / 4)), t = t0 + r < T ? t0 + r : t0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(o_at(r, c))),
+                     "l"(o + (bh * T + t) * (int64_t)DV + c), "r"(t0 + r < T ? 16 : 0)
+                     : "memory");
+    }
     copy_tile<DV, BQ, NTH * NG>(sG, dO + (bh * T + t0) * (int64_t)DV, T - t0);
     copy_tile<DK, BQ, NTH * NG>(sQ, q + (bh * T + t0) * (int64_t)DK, T - t0);
     send_v(g0);
     send_k(g0);
-    float L2[4], D[4], acc[4][DK / 16], out[4][DV / 16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < DV / 16; ++c) {
-            const int t = t0 + 4 * ty + i;
-            out[i][c] = t < T ? o[(bh * T + t) * (int64_t)DV + tx + 16 * c] : 0.f;
-        }
     copies_here<1>();
     __syncthreads();
+    if (threadIdx.x < BQ) {
+        const int r = threadIdx.x;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int d = 0; d < DV; d += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sG + r * ld<DV>() + d), y = *reinterpret_cast<const float4*>(o_at(r, d));
+            sum = fx::f2fma(make_float2(x.x, x.y), make_float2(y.x, y.y), sum);
+            sum = fx::f2fma(make_float2(x.z, x.w), make_float2(y.z, y.w), sum);
+        }
+        sO[r * LDP + BK] = sum.x + sum.y;  // in the row's pad
+        if (t0 + r < T) dbuf[bh * T + t0 + r] = sum.x + sum.y;
+    }
+    __syncthreads();
+    float L2[4], D[4], acc[4][DK / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, t = t0 + r;
-        float d = 0.f;
-#pragma unroll
-        for (int c = 0; c < DV / 16; ++c) d = fmaf(sG[r * ld<DV>() + tx + 16 * c], out[i][c], d);
-        D[i] = row_sum(d);
+        D[i] = sO[r * LDP + BK];
         L2[i] = t < T ? lse[bh * T + t] * kLog2e : INFINITY;  // rows past the end: p = 0
-        if (g0 == 0 && tx == 0 && t < T) dbuf[bh * T + t] = D[i];
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c) acc[i][c] = 0.f;
     }
