@@ -1,11 +1,13 @@
 """ctypes marshalling for librod.so. Argument checks and pointer passing only -- no arithmetic.
 
 Each function mirrors one entry point of include/rod.h and takes torch CUDA tensors in the
-layouts documented there. Outputs are allocated with torch when not supplied (plumbing);
+layouts documented there. Outputs are allocated with torch when not supplied (plumbing), on the
+stream that the call is given, to which they belong as tensors made under torch.cuda.stream do;
 the computation itself is entirely inside the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -122,6 +124,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call allocates its workspace and outputs: on the stream it is given, so that a block freed when the call
+    returns goes back to that stream's pool, and to no other stream's work while the kernels still use it."""
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
 def _need(t: torch.Tensor, name: str, dtype=None, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -181,12 +192,14 @@ def gla_prefill(q, k, v, g, state, o=None, chunk=64, workspace=None, stream=None
     if tuple(state.shape) != (B, H, dk, dv):
         raise ValueError("state must be [B,H,dk,dv]")
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 4)
     lib = load_library()
     ws_need = lib.rod_gla_prefill_workspace_size(B, H, T, dk, dv, chunk, _dtype_code(q))
     if ws_need and workspace is None:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib.rod_gla_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o),
                              B, H, T, dk, dv, chunk, _dtype_code(q), _ptr(workspace), ws_bytes,
@@ -211,7 +224,8 @@ def gla_prefill_noalloc(q, k, v, g, state, o=None, chunk=64, stream=None):
     if tuple(state.shape) != (B, H, dk, dv):
         raise ValueError("state must be [B,H,dk,dv]")
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 4)
     st = load_library().rod_gla_prefill_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
                                                 _ptr(o), B, H, T, dk, dv, chunk, _dtype_code(q),
@@ -232,7 +246,8 @@ def gla_decode_step(q, k, v, g, state, o=None, stream=None):
     if k.shape != q.shape or g.shape != q.shape or tuple(state.shape) != (N, H, dk, dv):
         raise ValueError("shape mismatch")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 3)
     st = load_library().rod_gla_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
                                             _ptr(o), N, H, dk, dv, _dtype_code(q), _stream(stream))
@@ -251,7 +266,8 @@ def swska_prefill(q, k, v, window, scale=None, o=None, stream=None):
     if tuple(k.shape) != (B, T, dk) or tuple(v.shape[:3]) != (B, H, T):
         raise ValueError("k must be [B,T,dk] and v [B,H,T,dv]")
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 4)
     st = load_library().rod_swska_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(o), B, H, T, dk, dv,
                                           int(window), float(scale or 0.0), _dtype_code(q),
@@ -270,10 +286,11 @@ def swska_prefill_lse(q, k, v, window, scale=None, o=None, lse=None, stream=None
     dv = v.shape[-1]
     if tuple(k.shape) != (B, T, dk) or tuple(v.shape[:3]) != (B, H, T):
         raise ValueError("k must be [B,T,dk] and v [B,H,T,dv]")
-    if o is None:
-        o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    with _on(stream):
+        if o is None:
+            o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     _need(o, "o", q.dtype, 4)
     _need(lse, "lse", torch.float32, 3)
     if tuple(o.shape) != (B, H, T, dv) or tuple(lse.shape) != (B, H, T):
@@ -300,7 +317,8 @@ def swska_decode(q, k_new, v_new, k_cache, v_cache, pos, window, scale=None, o=N
             or tuple(v_cache.shape) != (N, H, W, dv) or pos.shape[0] != N):
         raise ValueError("shape mismatch")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 3)
     st = load_library().rod_swska_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                          _ptr(v_cache), _ptr(pos), _ptr(o), N, H, dk, dv, W,
@@ -347,7 +365,8 @@ def swska_decode_paged(q, k_new, v_new, k_pool, v_pool, block_table, page_size, 
             or v_pool.shape[0] != k_pool.shape[0] or pos.shape[0] != N):
         raise ValueError("shape mismatch")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 3)
     st = load_library().rod_swska_decode_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
                                                _ptr(v_pool), _ptr(block_table), page, pps, _ptr(pos),
@@ -369,17 +388,19 @@ def gla_backward(q, k, v, g, dO, state0=None, dstate_final=None, workspace=None,
     if tuple(k.shape) != (B, H, T, dk) or tuple(g.shape) != (B, H, T, dk) or tuple(dO.shape) != (B, H, T, dv):
         raise ValueError("shape mismatch")
     if state0 is None:
-        state0 = torch.zeros(B, H, dk, dv, dtype=torch.float32, device=q.device)
+        with _on(stream):
+            state0 = torch.zeros(B, H, dk, dv, dtype=torch.float32, device=q.device)
     _need(state0, "state0", torch.float32, 4)
     if dstate_final is not None:
         _need(dstate_final, "dstate_final", torch.float32, 4)
     lib = load_library()
     need = lib.rod_gla_backward_workspace_size(B, H, T, dk, dv)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dg = torch.empty_like(g)
-    dS0 = torch.empty_like(state0)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dg = torch.empty_like(g)
+        dS0 = torch.empty_like(state0)
     st = lib.rod_gla_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state0), _ptr(dO),
                               None if dstate_final is None else _ptr(dstate_final), _ptr(dq),
                               _ptr(dk_), _ptr(dv_), _ptr(dg), _ptr(dS0), B, H, T, dk, dv,
@@ -401,9 +422,10 @@ def swska_backward(q, k, v, dO, window, scale=None, workspace=None, stream=None)
         raise ValueError("shape mismatch")
     lib = load_library()
     need = lib.rod_swska_backward_workspace_size(B, H, T)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     st = lib.rod_swska_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(dq), _ptr(dk_), _ptr(dv_),
                                 B, H, T, dk, dv, int(window), float(scale or 0.0), _dtype_code(q),
                                 _ptr(workspace), workspace.numel(), _stream(stream))
@@ -428,9 +450,10 @@ def swska_backward_lse(q, k, v, o, lse, dO, window, scale=None, workspace=None, 
         raise ValueError("shape mismatch")
     lib = load_library()
     need = lib.rod_swska_backward_workspace_size(B, H, T)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     st = lib.rod_swska_backward_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk_),
                                     _ptr(dv_), B, H, T, dk, dv, int(window), float(scale or 0.0), _dtype_code(q),
                                     _ptr(workspace), workspace.numel(), _stream(stream))
@@ -469,7 +492,8 @@ def swska_decode_fp8(q, k_new, v_new, k_cache, v_cache, pos, window, scale=None,
             or tuple(v_cache.shape) != (N, H, W, dv) or pos.shape[0] != N):
         raise ValueError("shape mismatch")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 3)
     st = load_library().rod_swska_decode_fp8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                              _ptr(v_cache), _ptr(pos), _ptr(o), N, H, dk, dv, W,
@@ -558,10 +582,11 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
     B, H, T, dk = _sizes(q, "q", 4)
     dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
-    if o is None:
-        o = torch.empty_like(v)
-    if lse is None:
-        lse = q.new_empty((B, H, T), dtype=torch.float32)
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(v)
+        if lse is None:
+            lse = q.new_empty((B, H, T), dtype=torch.float32)
     _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, (B, H, T, dv)), ("o", o, dt, (B, H, T, dv)),
             ("lse", lse, torch.float32, (B, H, T)))
     _raise_on("rod_swska_sink_prefill",
@@ -581,8 +606,9 @@ def swska_sink_backward(q, k, v, o, lse, dO, window, sinks, scale=None, workspac
     _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, rows), ("o", o, dt, rows), ("dO", dO, dt, rows),
             ("lse", lse, torch.float32, (B, H, T)))
     code, window, sinks = _dtype_code(q), int(window), int(sinks)
-    ws = _workspace(workspace, dev, "rod_swska_sink_backward_workspace_size", B, H, T, dk, dv, window, sinks)
-    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _on(stream):
+        ws = _workspace(workspace, dev, "rod_swska_sink_backward_workspace_size", B, H, T, dk, dv, window, sinks)
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     _raise_on("rod_swska_sink_backward",
               _launch(dev, stream, load_library().rod_swska_sink_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                       o.data_ptr(), lse.data_ptr(), dO.data_ptr(), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), B, H,
@@ -607,7 +633,8 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     N, max_pages = _sizes(block_table, "block_table", 2)
     dev, dt = _index(q, "q"), q.dtype
     if o is None:
-        o = q.new_empty((M, H, dv))
+        with _on(stream):
+            o = q.new_empty((M, H, dv))
     _expect(dev, ("q", q, dt, (M, H, dk)), ("k_pool", k_pool, dt, (P, page, dk)), ("v_pool", v_pool, dt, (P, H, page, dv)),
             ("block_table", block_table, torch.int32, (N, max_pages)), ("ctx", ctx, torch.int64, (N,)),
             ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,)), ("o", o, dt, (M, H, dv)))
@@ -625,7 +652,8 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     if most == 0:
         return o  # no sequence has a new token
     code = _dtype_code(q)
-    ws = _workspace(workspace, dev, "rod_swska_extend_paged_workspace_size", M, N, H, dk, dv, most, code)
+    with _on(stream):
+        ws = _workspace(workspace, dev, "rod_swska_extend_paged_workspace_size", M, N, H, dk, dv, most, code)
     _raise_on("rod_swska_extend_paged",
               _launch(dev, stream, load_library().rod_swska_extend_paged, q.data_ptr(), new[0], new[1],
                       k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), new[2], cu_seqlens.data_ptr(),
@@ -648,10 +676,11 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     dev, i32 = _index(ctx, "ctx"), torch.int32
     if M < 0:
         raise ValueError("max_tokens must not be negative")
-    if cu_seqlens is None:
-        cu_seqlens = first.new_empty(N + 1)
-    if slot_map is None:
-        slot_map = first.new_empty(M)
+    with _on(stream):
+        if cu_seqlens is None:
+            cu_seqlens = first.new_empty(N + 1)
+        if slot_map is None:
+            slot_map = first.new_empty(M)
     _expect(dev, ("ctx", ctx, torch.int64, (N,)), ("n_new", n_new, i32, (N,)),
             ("block_table", block_table, i32, (N, max_pages)), ("first", first, i32, (N,)),
             ("free_list", free_list, i32, (P,)), ("free_count", free_count, i32, (1,)),

@@ -41,3 +41,66 @@ def test_first_row_in_fp32(T, dk, dv, W, S):
     rod.check()
     assert (got["dq"][:, :, 0] == 0).all() and not (got["dq"][:, :, 1:] == 0).all(-1).any()
     _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"T{T}")
+
+
+# ---- a stream given by the caller -----------------------------------------------------------------------------
+def _late(stream, ms=20):
+    """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 1.5e6))
+
+
+def _overwrite(sizes):
+    """Blocks of these sizes on the current stream, as any later work there may take them, filled with NaN bits."""
+    return [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+
+
+def test_training_step_on_a_stream_keeps_its_workspace():
+    """Without a workspace the call takes one from the stream it runs on: work that the current stream starts after the call
+    has returned does not get that block, nor that of an output which the caller has dropped."""
+    B, H, T, W, S = 1, 4, 1500, 300, 4
+    q, k, v = wl.swska_inputs(B, H, T, 128, 128, seed=31, device=DEV)
+    dO = torch.randn_like(v)
+    want = _step(q, k, v, dO, W, S)
+    n = rod.load_library().rod_swska_sink_backward_workspace_size(B, H, T, 128, 128, W, S)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        _late(side)
+        got = _step(q, k, v, dO, W, S, stream=side)
+        _overwrite([n, n // 2, v.numel() * 2, q.numel() * 2, k.numel() * 2, B * H * T * 4])
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[x], want[x]) for x in got)
+    o, lse = rod.swska_prefill_lse(q, k, v, W)
+    old = rod.swska_backward_lse(q, k, v, o, lse, dO, W)
+    n = rod.load_library().rod_swska_backward_workspace_size(B, H, T)
+    torch.cuda.synchronize()
+    _late(side)
+    got = rod.swska_backward_lse(q, k, v, o, lse, dO, W, stream=side)
+    _overwrite([n, n // 2, v.numel() * 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, old))
+
+
+def test_extend_on_two_streams_with_workspaces_of_their_own():
+    """Two calls at once on two streams, each without a workspace, and work on the current stream behind them."""
+    a = ref.Batch("bf16", 6, 128, 128, 200, 4, 16, [50, 700, 0, 333], [1, 300, 2, 90], seed=1)
+    b = ref.Batch("bf16", 6, 128, 128, 200, 4, 16, [500, 70, 9, 33], [200, 1, 0, 16], seed=2)
+    batches = []
+    for x in (a, b):
+        args = x.args(DEV)
+        o = x.o.to(DEV)
+        rod.swska_extend_paged(*args, x.W, sinks=x.S, o=o)
+        n = rod.load_library().rod_swska_extend_paged_workspace_size(x.q.shape[0], len(x.ctx), x.H, 128, 128, x.q.shape[0], rod.ROD_BF16)
+        batches.append((x, args, o, n, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        outs = []
+        for x, args, o, n, s in batches:
+            _late(s)
+            outs.append(rod.swska_extend_paged(*args, x.W, sinks=x.S, stream=s))
+        _overwrite([n for _, _, _, n, _ in batches] + [o.numel() * 2 for _, _, o, _, _ in batches])
+        torch.cuda.synchronize()
+        rod.check()
+        for (x, args, o, n, s), got in zip(batches, outs):
+            assert torch.equal(got, o)
