@@ -151,7 +151,8 @@ int device_sm_count();
 cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes);
 
 // A launch that may begin while the one before it on the stream ends (once all CTAs of that one have
-// allowed it); the kernel itself waits for that end before it reads what the other wrote.
+// allowed it); the kernel itself waits for that end before it reads what the other wrote, by __ldcg or asynchronous copies
+// through pointers that are not __restrict__ (the compiler may move a load of what nothing writes above the wait).
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchAttribute at[1];

@@ -16,7 +16,7 @@ sink_reduce_kernel(const SinkParts p, void* __restrict__ dk, void* __restrict__ 
          i += (int64_t)gridDim.x * blockDim.x) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](const float* x) {
-            const float4 t = *reinterpret_cast<const float4*>(x);
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(x));
             s.x += t.x;
             s.y += t.y;
             s.z += t.z;

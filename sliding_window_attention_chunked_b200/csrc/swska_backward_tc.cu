@@ -187,8 +187,8 @@ template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  __nv_bfloat16* __restrict__ dq, const float* __restrict__ nlse2,
-                  float* __restrict__ dbuf, int T, int Tpad, int H, int W, float scale_log2,
+                  __nv_bfloat16* __restrict__ dq, const float* nlse2,
+                  float* dbuf, int T, int Tpad, int H, int W, float scale_log2,
                   float scale, int n_qtiles, int S_arg) {
     using namespace qa;
     // the key-tile kernel may set itself up on SMs that fall free; it waits for this launch's end
@@ -382,8 +382,8 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t tQ = tmem + lane_base + 256u + 64u * w;
         const int t = t0 + row;
         if (SINK) asm volatile("griddepcontrol.wait;" ::: "memory");  // the row statistics
-        const float nL = nlse2[(int64_t)bh * Tpad + t];  // -inf past the end: p = 0
-        float Dr = dbuf[(int64_t)bh * Tpad + t];
+        const float nL = __ldcg(nlse2 + (int64_t)bh * Tpad + t);  // -inf past the end: p = 0
+        float Dr = __ldcg(dbuf + (int64_t)bh * Tpad + t);
         const float2 sl2 = make_float2(scale_log2, scale_log2), nl2 = make_float2(nL, nL);
         float2 d2 = make_float2(Dr, Dr);
         float2 e2 = make_float2(0.f, 0.f);  // SINK: sum of dS
@@ -524,7 +524,7 @@ template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS_KEY, 1)
 ska_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const float* __restrict__ nlse2, const float* __restrict__ dbuf,
+                    const float* nlse2, const float* dbuf,
                     __nv_bfloat16* __restrict__ dv, float* __restrict__ dk_part, int B, int T, int Tpad,
                     int H, int HG, int W, float scale_log2, int n_qtiles, int S_arg, const SinkParts parts) {
     using namespace ka;

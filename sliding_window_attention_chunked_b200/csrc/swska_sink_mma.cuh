@@ -363,7 +363,7 @@ template <int DK, int DV> constexpr int dkv_smem() { return 3 * (tile_bytes<DK>(
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
-                    const float* __restrict__ lse, const float* __restrict__ dbuf, const bf16_t* __restrict__ dO,
+                    const float* __restrict__ lse, const float* dbuf, const bf16_t* __restrict__ dO,
                     bf16_t* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that adds the parts waits for the end
     extern __shared__ __align__(16) unsigned char sm[];
@@ -385,7 +385,7 @@ sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, 
             copy_tile<DK>(stage + s * STAGE, qb, qt * R, T);
             copy_tile<DV>(stage + s * STAGE + tile_bytes<DK>(), gb, qt * R, T);
             if (threadIdx.x < R) stats[2 * R * s + r] = row < T ? lse[bh * T + row] * kLog2e : INFINITY;
-            else stats[2 * R * s + R + r] = row < T ? dbuf[bh * T + row] : 0.f;
+            else stats[2 * R * s + R + r] = row < T ? __ldcg(dbuf + bh * T + row) : 0.f;
         }
         copies_done();
     };

@@ -326,7 +326,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dkv<DK, DV>::NG)
 sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                const float* __restrict__ lse, const float* __restrict__ dbuf, const float* __restrict__ dO,
+                const float* __restrict__ lse, const float* dbuf, const float* __restrict__ dO,
                 float* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
     constexpr int NG = Dkv<DK, DV>::NG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that adds the parts waits for the end
