@@ -83,7 +83,8 @@ __device__ __forceinline__ Range range_of(const TableArgs& a, int64_t c, int m, 
     const unsigned page = (unsigned)a.page, cap = 1u << 31;
     c = c < (1ll << 32) ? c : (1ll << 32);
     auto clamp = [&](int64_t x) { return x < 0 ? 0u : (x < (int64_t)cap ? (unsigned)x : cap); };
-    const int sp = (a.S + a.page - 1) / a.page;
+    const unsigned whole = (unsigned)a.S / page + ((unsigned)a.S % page != 0);  // S + page may pass 2^31
+    const int sp = (int)(whole < (unsigned)a.max_pages ? whole : (unsigned)a.max_pages);
     const unsigned used = clamp(c) / page + (clamp(c) % page != 0);
     const unsigned end = clamp(c + m) / page + (clamp(c + m) % page != 0);
     unsigned low = clamp(c - a.W + 1) / page;

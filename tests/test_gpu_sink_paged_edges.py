@@ -43,6 +43,27 @@ def test_first_row_in_fp32(T, dk, dv, W, S):
     _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"T{T}")
 
 
+# ---- page tables: first tokens beyond every page ------------------------------------------------------------
+@pytest.mark.parametrize("S", [5 * 64, 10 ** 9, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1])
+@pytest.mark.parametrize("ps", [64, 1, 24])
+def test_page_tables_keep_all_first_tokens(S, ps):
+    """`sinks` past every position keeps every page of a running sequence, however large it is."""
+    N, mp, P, W, M = 3, 8, 30, 16, 200
+    ctx, new = [5 * ps, 3 * ps + ps // 2, 7 * ps], [ps, 1, -1]
+    table, free = [[-1] * mp for _ in range(N)], list(range(P))
+    for n in range(N):
+        for p in range(-(-ctx[n] // ps)):
+            table[n][p] = free.pop()
+    top = len(free)
+    args = (ctx, new, table, [0] * N, free + [-1] * (P - top), top, ps, W, S, M)
+    dev = lambda x, dt=torch.int32: torch.tensor(x, dtype=dt, device=DEV)
+    t, f, fl, fc = dev(table), dev([0] * N), dev(args[4]), dev([top])
+    cu, slot = rod.swska_page_tables(dev(ctx, torch.int64), dev(new), t, f, fl, fc, ps, W, S, M)
+    rod.check()
+    for x, y in zip((t.tolist(), f.tolist(), fl.tolist(), int(fc), cu.tolist(), slot.tolist()), ref.page_tables(*args)):
+        assert x == (y if isinstance(y, int) else list(y))
+
+
 # ---- a stream given by the caller -----------------------------------------------------------------------------
 def _late(stream, ms=20):
     """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
