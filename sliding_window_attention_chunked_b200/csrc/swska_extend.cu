@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(NT) extend_prepare_kernel(const ExtendArgs a, 
             }
             if (all.v < 0x7fffffff) break;
         }
-        // Rows of two sequences at once (cu_seqlens that falls) could make more query tiles than there is
-        // room for: then nothing is computed
-        if (all.items > r.cap_items) {
+        // No query tile for this route: nothing to divide. Rows of two sequences at once (cu_seqlens that falls) could
+        // make more query tiles than there is room for: then nothing is computed
+        if (all.items == 0 || all.items > r.cap_items) {
             for (int c = threadIdx.x; c < r.cols; c += NT) reinterpret_cast<int2*>(r.range)[c] = make_int2(1, 0);
             return;
         }

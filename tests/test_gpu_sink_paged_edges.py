@@ -64,6 +64,55 @@ def test_page_tables_keep_all_first_tokens(S, ps):
         assert x == (y if isinstance(y, int) else list(y))
 
 
+# ---- paged attention: many sequences, routes without work --------------------------------------------------------
+def _paged(b, **kw):
+    args, o = b.args(DEV), b.o.to(DEV)
+    rod.swska_extend_paged(*args, b.W, sinks=b.S, o=o, **kw)
+    return o, args
+
+
+def _check_paged(b, what, **kw):
+    """Rows, the padding behind them and the cache against the 64-bit reference."""
+    o, args = _paged(b, **kw)
+    rod.check()
+    r, ra, kr, vr = b.reference()
+    ref.check(o.cpu(), r, ra, b.terms(), b.dk, ref.amp(b.q, torch.nan_to_num(b.k_pool)), what)
+    rows = int(b.cu[-1])
+    assert torch.equal(o[rows:].cpu(), b.o[rows:]), f"{what}: padding"
+    for x, y in ((args[3], kr), (args[4], vr)):
+        assert torch.equal(torch.nan_to_num(x.float().cpu(), 1234.5), torch.nan_to_num(y.float(), 1234.5)), f"{what}: cache"
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("fp32", 16, 32)])
+@pytest.mark.parametrize("N,pattern", [(257, "ends"), (600, "idle block"), (513, "mixed"), (1030, "last"), (300, "none long")])
+def test_extend_many_sequences(N, pattern, dtype, dk, dv):
+    """More sequences than the 256 that are divided at a time: idle runs over the edges of such blocks, a block without a token,
+    short and long sequences side by side."""
+    lens = {"ends": lambda n: 1 if 200 <= n % 256 else 0, "idle block": lambda n: 0 if n < 256 else n % 3, "mixed": lambda n: (0, 20, 3)[n % 3],
+            "last": lambda n: 60 if n == N - 1 else 0, "none long": lambda n: 1 + n % 2}[pattern]
+    b = ref.Batch(dtype, 2, dk, dv, 40, 4, 16, [(37 * n) % 90 for n in range(N)], [lens(n) for n in range(N)], pad=3, seed=N)
+    _check_paged(b, f"{N} {pattern}")
+    _check_paged(b, f"{N} {pattern} bounded", max_len=b.max_len)
+
+
+@pytest.mark.parametrize("lens", [[3, 16, 1, 0], [40, 0, 17], [0, 0, 0]])
+def test_extend_a_route_without_work(lens):
+    """The bound on the lengths allows both kernels, the lengths give one of them nothing (or neither anything)."""
+    b = ref.Batch("bf16", 5, 128, 128, 70, 4, 24, [100, 7, 300, 0][:len(lens)], lens, pad=25, seed=sum(lens))
+    _check_paged(b, f"{lens}")
+    _check_paged(b, f"{lens} bounded", max_len=40)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_extend_missing_pages_and_rows_behind(dtype):
+    """Pages that the table lacks are left out, the rows of the sequences around them are right, the padding keeps what it holds."""
+    b = ref.Batch(dtype, 3, 128, 128, 60, 4, 16, [100, 40, 0, 20], [1, 20, 5, 2], pad=4, seed=1)
+    b.table[1, 1], b.table[0, 0] = -1, b.P
+    b.k_pool.nan_to_num_(0.5)
+    b.v_pool.nan_to_num_(0.25)
+    _check_paged(b, "missing")
+
+
 # ---- a stream given by the caller -----------------------------------------------------------------------------
 def _late(stream, ms=20):
     """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
