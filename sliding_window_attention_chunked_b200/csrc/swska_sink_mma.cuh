@@ -359,7 +359,7 @@ sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, c
 // ---- dk (one part per head), dv ----------------------------------------------------------------------
 template <int DK, int DV> constexpr int dkv_smem() { return 3 * (tile_bytes<DK>() + tile_bytes<DV>()) + 2 * 2 * R * 4; }
 
-// blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
+// blockIdx.x: for each sequence and head, its key tiles, then (tile s, segment g) of the first tokens' far queries
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH, DK + DV <= 128 ? 3 : 1)
 sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, const bf16_t* __restrict__ v,
@@ -370,10 +370,11 @@ sink_mma_dkv_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, 
     constexpr int STAGE = tile_bytes<DK>() + tile_bytes<DV>();
     const uint32_t sK = smem_u32(sm), sV = sK + tile_bytes<DK>(), stage = sK + STAGE;
     float* stats = reinterpret_cast<float*>(sm + 3 * STAGE);  // per stage: 64 log-sum-exps, 64 D
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int64_t bh = (int64_t)b * H + h;
+    const int tiles = parts.ctas();
+    const int64_t bh = blockIdx.x / tiles;
+    const int b = (int)bh / H, h = (int)bh - b * H;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c2 = 2 * (lane % 4);
-    const SinkWork w = parts.work((int)blockIdx.x);
+    const SinkWork w = parts.work((int)blockIdx.x - (int)bh * tiles);
     const int key0 = w.tile * R, key = key0 + 16 * warp + lane / 4;  // this thread's rows: key, key + 8
     const float scale_log2 = scale * kLog2e;
     const bf16_t *qb = q + bh * T * DK, *gb = dO + bh * T * DV;
@@ -473,10 +474,10 @@ template <int DK, int DV>
 cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     constexpr int q_smem = dq_smem<DK, DV>(), kv_smem = dkv_smem<DK, DV>();
     const int qtiles = (a.T + R - 1) / R;
-    const int64_t grid = (int64_t)qtiles * a.B * a.H;
-    if (grid > 0x7fffffffLL || a.B > 65535) return cudaErrorInvalidConfiguration;
     SinkParts parts = sink_parts_plan(a, R, R, a.H);
     float* dbuf = sink_parts_bind(parts, a);
+    const int64_t grid = (int64_t)qtiles * a.B * a.H, key_grid = (int64_t)parts.ctas() * a.B * a.H;
+    if (grid > 0x7fffffffLL || key_grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e;
     static std::atomic<uint64_t> q_set{0}, k_set{0};
     if ((e = allow_smem(q_set, (const void*)sink_mma_dq_kernel<DK, DV>, q_smem)) != cudaSuccess) return e;
@@ -486,7 +487,7 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     sink_mma_dq_kernel<DK, DV><<<(unsigned)grid, NTH, q_smem, s>>>(q, k, v, static_cast<const bf16_t*>(a.o), a.lse, dO, static_cast<bf16_t*>(a.dq), dbuf, a.H, a.T,
                                                                   a.W, a.S, a.scale, a.grad_scale, qtiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_overlapped(sink_mma_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH), kv_smem,
+    e = launch_overlapped(sink_mma_dkv_kernel<DK, DV>, dim3((unsigned)key_grid), dim3(NTH), kv_smem,
                           s, q, k, v, a.lse, static_cast<const float*>(dbuf), dO, static_cast<bf16_t*>(a.dv), parts, a.B, a.H, a.T,
                           a.W, a.S, a.scale);
     note_launches(2);

@@ -322,7 +322,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
     }
 }
 
-// blockIdx.x: a key tile, or past them (tile s, segment g) of the first tokens' far queries
+// blockIdx.x: for each sequence and head, its key tiles, then (tile s, segment g) of the first tokens' far queries
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dkv<DK, DV>::NG)
 sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
@@ -340,10 +340,11 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     float* sP = sG + BK * ld<DV>();
     float* sL = sP + BQ * LDP;
     float* sD = sL + BK;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int64_t bh = (int64_t)b * H + h;
+    const int tiles = parts.ctas();
+    const int64_t bh = blockIdx.x / tiles;
+    const int b = (int)bh / H, h = (int)bh - b * H;
     const int tx = tid % 16, ty = tid / 16;
-    const SinkWork w = parts.work((int)blockIdx.x);
+    const SinkWork w = parts.work((int)blockIdx.x - (int)bh * tiles);
     const int key0 = w.tile * BQ;
     auto send_g = [&](int qt) {
         const int t0 = qt * BK;
@@ -462,10 +463,10 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     using Q = Dq<DK, DV>;
     using K = Dkv<DK, DV>;
     const int qtiles = (a.T + BQ - 1) / BQ;
-    const int64_t grid = (int64_t)qtiles * a.B * a.H;
-    if (grid > 0x7fffffffLL || a.B > 65535) return cudaErrorInvalidConfiguration;
     SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
+    const int64_t grid = (int64_t)qtiles * a.B * a.H, key_grid = (int64_t)parts.ctas() * a.B * a.H;
+    if (grid > 0x7fffffffLL || key_grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e;
     static std::atomic<uint64_t> q_set{0}, k_set{0};
     if ((e = allow_smem(q_set, (const void*)sink_dq_kernel<DK, DV>, Q::smem)) != cudaSuccess) return e;
@@ -473,7 +474,7 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
         f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_overlapped(sink_dkv_kernel<DK, DV>, dim3((unsigned)parts.ctas(), (unsigned)a.H, (unsigned)a.B), dim3(NTH * K::NG),
+    e = launch_overlapped(sink_dkv_kernel<DK, DV>, dim3((unsigned)key_grid), dim3(NTH * K::NG),
                           K::smem, s, f32(a.q), f32(a.k), f32(a.v), a.lse, static_cast<const float*>(dbuf), f32(a.dO),
                           static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
     note_launches(2);

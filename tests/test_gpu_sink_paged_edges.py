@@ -43,6 +43,22 @@ def test_first_row_in_fp32(T, dk, dv, W, S):
     _check_step(got, ref.train(q, k, v, dO, W, S), q, k, W, S, what=f"T{T}")
 
 
+# ---- many sequences -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_training_step_of_many_short_sequences(dtype):
+    """More than 65535 sequences: the backward takes every batch that the forward takes."""
+    B, H, T, d, W, S = 65537, 1, 2, 16, 2, 1
+    q, k, v = wl.swska_inputs(B, H, T, d, d, seed=9, dtype=dtype, device=DEV)
+    dO = torch.randn(B, H, T, d, device=DEV).to(DT[dtype])
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    at = torch.tensor([0, 1, 32768, 65534, 65535, 65536], device=DEV)
+    part = lambda x: x[at]
+    _check_step({n: part(x) for n, x in got.items()}, ref.train(*map(part, (q, k, v, dO)), W, S), part(q), part(k), W, S, what="many")
+    same = _step(*(x[:9000].contiguous() for x in (q, k, v, dO)), W, S)
+    assert all(torch.equal(same[n], got[n][:9000]) for n in same)
+
+
 # ---- page tables: first tokens beyond every page ------------------------------------------------------------
 @pytest.mark.parametrize("S", [5 * 64, 10 ** 9, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1])
 @pytest.mark.parametrize("ps", [64, 1, 24])
