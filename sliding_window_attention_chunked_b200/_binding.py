@@ -625,7 +625,7 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     n's tokens at positions ctx[n], ctx[n]+1, ...; k_pool [P,page,dk], v_pool [P,H,page,dv];
     block_table [N,max_pages] int32 (-1: no page); slot_map [M] int32 (-1: not written); cu_seqlens
     [N+1] int32; ctx [N] int64. Query at position p sees keys j <= p with j > p - window or
-    j < sinks. max_len: a bound on the new tokens of one sequence (default M). k_new, v_new and
+    j < sinks. max_len: a bound on the new tokens of one sequence (default M, and so is 0). k_new, v_new and
     slot_map may all be None: the cache has the tokens. Returns o [M,H,dv]; rows past
     cu_seqlens[N] are not written. The tables come from swska_page_tables."""
     M, H, dk = _sizes(q, "q", 3)
@@ -649,8 +649,6 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     most = M if max_len is None else int(max_len)
     if most < 0:
         raise ValueError("max_len must not be negative")
-    if most == 0:
-        return o  # no sequence has a new token
     code = _dtype_code(q)
     with _on(stream):
         ws = _workspace(workspace, dev, "rod_swska_extend_paged_workspace_size", M, N, H, dk, dv, most, code)

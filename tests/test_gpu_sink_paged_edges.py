@@ -129,6 +129,16 @@ def test_extend_missing_pages_and_rows_behind(dtype):
     _check_paged(b, "missing")
 
 
+def test_extend_bound_of_zero_is_no_bound():
+    """max_len = 0 stands for M, as at the C entry: the new tokens are written and attended to."""
+    b = ref.Batch("bf16", 3, 128, 128, 60, 4, 16, [100, 3], [2, 20], pad=3, seed=8)
+    _check_paged(b, "max_len 0", max_len=0)
+    none = ref.Batch("bf16", 3, 128, 128, 60, 4, 16, [100, 3], [0, 0], pad=2, seed=8)
+    _check_paged(none, "no tokens", max_len=0)
+    args = none.args(DEV)
+    assert rod.swska_extend_paged(args[0][:0], *(a[:0] for a in args[1:3]), *args[3:6], args[6][:0], *args[7:], 60, max_len=0).shape == (0, 3, 128)
+
+
 # ---- a stream given by the caller -----------------------------------------------------------------------------
 def _late(stream, ms=20):
     """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
