@@ -146,6 +146,14 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
+def _int32(x, name: str) -> int:
+    """A number that the C entry takes as an int (ctypes keeps the low 32 bits of a larger one without a word)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must be below 2^31, got {x}")
+    return x
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype not in _DT:
         raise ValueError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
@@ -270,7 +278,7 @@ def swska_prefill(q, k, v, window, scale=None, o=None, stream=None):
             o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
     _need(o, "o", q.dtype, 4)
     st = load_library().rod_swska_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(o), B, H, T, dk, dv,
-                                          int(window), float(scale or 0.0), _dtype_code(q),
+                                          _int32(window, "window"), float(scale or 0.0), _dtype_code(q),
                                           _stream(stream))
     _raise_on("rod_swska_prefill", st)
     return o
@@ -296,7 +304,7 @@ def swska_prefill_lse(q, k, v, window, scale=None, o=None, lse=None, stream=None
     if tuple(o.shape) != (B, H, T, dv) or tuple(lse.shape) != (B, H, T):
         raise ValueError("o must be [B,H,T,dv] and lse [B,H,T]")
     st = load_library().rod_swska_prefill_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, dk, dv,
-                                              int(window), float(scale or 0.0), _dtype_code(q), _stream(stream))
+                                              _int32(window, "window"), float(scale or 0.0), _dtype_code(q), _stream(stream))
     _raise_on("rod_swska_prefill_lse", st)
     return o, lse
 
@@ -427,7 +435,7 @@ def swska_backward(q, k, v, dO, window, scale=None, workspace=None, stream=None)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     st = lib.rod_swska_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(dq), _ptr(dk_), _ptr(dv_),
-                                B, H, T, dk, dv, int(window), float(scale or 0.0), _dtype_code(q),
+                                B, H, T, dk, dv, _int32(window, "window"), float(scale or 0.0), _dtype_code(q),
                                 _ptr(workspace), workspace.numel(), _stream(stream))
     _raise_on("rod_swska_backward", st)
     return dq, dk_, dv_
@@ -455,7 +463,7 @@ def swska_backward_lse(q, k, v, o, lse, dO, window, scale=None, workspace=None, 
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     st = lib.rod_swska_backward_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk_),
-                                    _ptr(dv_), B, H, T, dk, dv, int(window), float(scale or 0.0), _dtype_code(q),
+                                    _ptr(dv_), B, H, T, dk, dv, _int32(window, "window"), float(scale or 0.0), _dtype_code(q),
                                     _ptr(workspace), workspace.numel(), _stream(stream))
     _raise_on("rod_swska_backward_lse", st)
     return dq, dk_, dv_
@@ -579,6 +587,7 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
     """swska_prefill_lse whose first ``sinks`` tokens (0 .. 128) stay visible to every later query:
     q [B,H,T,dk], k [B,T,dk] (shared by the heads), v [B,H,T,dv]. Returns (o [B,H,T,dv],
     lse [B,H,T] fp32), the pair swska_sink_backward takes."""
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
     B, H, T, dk = _sizes(q, "q", 4)
     dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
@@ -591,7 +600,7 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
             ("lse", lse, torch.float32, (B, H, T)))
     _raise_on("rod_swska_sink_prefill",
               _launch(dev, stream, load_library().rod_swska_sink_prefill, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                      o.data_ptr(), lse.data_ptr(), B, H, T, dk, dv, int(window), int(sinks), float(scale or 0.0),
+                      o.data_ptr(), lse.data_ptr(), B, H, T, dk, dv, window, sinks, float(scale or 0.0),
                       _dtype_code(q)))
     return o, lse
 
@@ -599,13 +608,14 @@ def swska_sink_prefill(q, k, v, window, sinks, scale=None, o=None, lse=None, str
 def swska_sink_backward(q, k, v, o, lse, dO, window, sinks, scale=None, workspace=None, stream=None):
     """Gradients of swska_sink_prefill from its o and lse (same q, k, v, window, sinks and scale) and
     the loss gradient dO [B,H,T,dv]. Returns (dq, dk, dv) in the layouts and dtype of q, k, v."""
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
     B, H, T, dk = _sizes(q, "q", 4)
     dv = _sizes(v, "v", 4)[3]
     dev, dt = _index(q, "q"), q.dtype
     rows = (B, H, T, dv)
     _expect(dev, ("q", q, dt, (B, H, T, dk)), ("k", k, dt, (B, T, dk)), ("v", v, dt, rows), ("o", o, dt, rows), ("dO", dO, dt, rows),
             ("lse", lse, torch.float32, (B, H, T)))
-    code, window, sinks = _dtype_code(q), int(window), int(sinks)
+    code = _dtype_code(q)
     with _on(stream):
         ws = _workspace(workspace, dev, "rod_swska_sink_backward_workspace_size", B, H, T, dk, dv, window, sinks)
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -628,6 +638,7 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     j < sinks. max_len: a bound on the new tokens of one sequence (default M, and so is 0). k_new, v_new and
     slot_map may all be None: the cache has the tokens. Returns o [M,H,dv]; rows past
     cu_seqlens[N] are not written. The tables come from swska_page_tables."""
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
     M, H, dk = _sizes(q, "q", 3)
     P, _, page, dv = _sizes(v_pool, "v_pool", 4)
     N, max_pages = _sizes(block_table, "block_table", 2)
@@ -646,7 +657,7 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
         new = None, None, None
     else:
         raise ValueError("k_new, v_new and slot_map come together or not at all")
-    most = M if max_len is None else int(max_len)
+    most = M if max_len is None else _int32(max_len, "max_len")
     if most < 0:
         raise ValueError("max_len must not be negative")
     code = _dtype_code(q)
@@ -655,7 +666,7 @@ def swska_extend_paged(q, k_new, v_new, k_pool, v_pool, block_table, slot_map, c
     _raise_on("rod_swska_extend_paged",
               _launch(dev, stream, load_library().rod_swska_extend_paged, q.data_ptr(), new[0], new[1],
                       k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), new[2], cu_seqlens.data_ptr(),
-                      ctx.data_ptr(), o.data_ptr(), M, N, H, dk, dv, P, page, max_pages, int(window), int(sinks), most,
+                      ctx.data_ptr(), o.data_ptr(), M, N, H, dk, dv, P, page, max_pages, window, sinks, most,
                       float(scale or 0.0), code, ws.data_ptr(), ws.numel() * ws.element_size()))
     return o
 
@@ -668,8 +679,9 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     (past the first ``sinks`` tokens) go back to the free list, pages for the new tokens are taken
     from it. Returns (cu_seqlens [N+1], slot_map [max_tokens]) int32 for swska_extend_paged; a
     sequence for which pages or tokens run out is served none this step."""
+    page_size, window, sinks = _int32(page_size, "page_size"), _int32(window, "window"), _int32(sinks, "sinks")
     N, max_pages = _sizes(block_table, "block_table", 2)
-    P, M = _sizes(free_list, "free_list", 1)[0], int(max_tokens)
+    P, M = _sizes(free_list, "free_list", 1)[0], _int32(max_tokens, "max_tokens")
     _sizes(ctx, "ctx", 1)
     dev, i32 = _index(ctx, "ctx"), torch.int32
     if M < 0:
@@ -686,6 +698,5 @@ def swska_page_tables(ctx, n_new, block_table, first, free_list, free_count, pag
     _raise_on("rod_swska_page_tables",
               _launch(dev, stream, load_library().rod_swska_page_tables, ctx.data_ptr(), n_new.data_ptr(),
                       block_table.data_ptr(), first.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
-                      cu_seqlens.data_ptr(), slot_map.data_ptr(), N, max_pages, P, int(page_size), int(window),
-                      int(sinks), M))
+                      cu_seqlens.data_ptr(), slot_map.data_ptr(), N, max_pages, P, page_size, window, sinks, M))
     return cu_seqlens, slot_map
