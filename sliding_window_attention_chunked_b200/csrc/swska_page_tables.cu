@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(NT, 1) page_tables_kernel(const TableArgs a) {
                 --left;
             }
         }
-        if (i0 + 4 <= a.M) {
+        if (a.M - i0 >= 4) {  // i0 + 4 may pass 2^31
             *reinterpret_cast<int4*>(a.slot + i0) = make_int4(out[0], out[1], out[2], out[3]);
         } else {
             for (int u = 0; i0 + u < a.M; ++u) a.slot[i0 + u] = out[u];

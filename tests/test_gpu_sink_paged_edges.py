@@ -80,6 +80,19 @@ def test_page_tables_keep_all_first_tokens(S, ps):
         assert x == (y if isinstance(y, int) else list(y))
 
 
+def test_page_tables_largest_slot_map():
+    """A slot map of 2^31 - 1 tokens is filled to its end and no further."""
+    M, i32 = 2 ** 31 - 1, lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    buf = torch.full((M + 5,), 7, dtype=torch.int32, device=DEV)
+    table, free, count = torch.full((1, 4), -1, dtype=torch.int32, device=DEV), i32(3, 1, 0, 2), i32(4)
+    cu, slot = rod.swska_page_tables(torch.zeros(1, dtype=torch.int64, device=DEV), i32(20), table, i32(0), free, count, 16, 8, 0, M, slot_map=buf[:M])
+    rod.check()
+    assert cu.tolist() == [0, 20] and slot[:20].tolist() == [*range(32, 48), *range(0, 4)]
+    assert (buf[M:] == 7).all()
+    # everything past the tokens is -1 (in pieces: a comparison of the whole takes as much memory again)
+    assert all(int((x != -1).sum()) == 0 for x in slot[20:].split(2 ** 28))
+
+
 # ---- paged attention: many sequences, routes without work --------------------------------------------------------
 def _paged(b, **kw):
     args, o = b.args(DEV), b.o.to(DEV)
