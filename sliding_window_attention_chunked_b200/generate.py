@@ -63,17 +63,18 @@ class MixerStack:
         ring buffers (last W tokens, slot = position mod W) ready for decode, and sets the next
         position to T. Returns the prefill outputs [N,H,T,d] per layer."""
         outs, T = [], None
-        for l, (lay, ins) in enumerate(zip(self.layers, inputs)):
-            if self.kind(l) == "gla":
-                q, k, v, g = ins
-                lay["state"].zero_()
-                outs.append(rod.gla_prefill(q, k, v, g, lay["state"], chunk=chunk, stream=stream))
-            else:
-                q, k, v = ins
-                outs.append(rod.swska_prefill(q, k, v, self.W, stream=stream))
-                rod.swska_cache_fill(k, v, lay["k_cache"], lay["v_cache"], self.W, stream=stream)
-            T = q.shape[2]
-        self.pos.fill_(int(T or 0))
+        with rod._on(stream):
+            for l, (lay, ins) in enumerate(zip(self.layers, inputs)):
+                if self.kind(l) == "gla":
+                    q, k, v, g = ins
+                    lay["state"].zero_()
+                    outs.append(rod.gla_prefill(q, k, v, g, lay["state"], chunk=chunk, stream=stream))
+                else:
+                    q, k, v = ins
+                    outs.append(rod.swska_prefill(q, k, v, self.W, stream=stream))
+                    rod.swska_cache_fill(k, v, lay["k_cache"], lay["v_cache"], self.W, stream=stream)
+                T = q.shape[2]
+            self.pos.fill_(int(T or 0))
         return outs
 
     # ---- decode ----------------------------------------------------------------------------
@@ -88,14 +89,15 @@ class MixerStack:
 
     def step_eager(self, stream=None):
         """One decode token for every sequence through every layer, then position + 1."""
-        for l, lay in enumerate(self.layers):
-            if self.kind(l) == "gla":
-                rod.gla_decode_step(lay["q"], lay["k"], lay["v"], lay["g"], lay["state"], o=lay["o"],
-                                    stream=stream)
-            else:
-                rod.swska_decode(lay["q"], lay["k_new"], lay["v_new"], lay["k_cache"], lay["v_cache"],
-                                 self.pos, self.W, o=lay["o"], stream=stream)
-        self.pos.add_(1)
+        with rod._on(stream):
+            for l, lay in enumerate(self.layers):
+                if self.kind(l) == "gla":
+                    rod.gla_decode_step(lay["q"], lay["k"], lay["v"], lay["g"], lay["state"], o=lay["o"],
+                                        stream=stream)
+                else:
+                    rod.swska_decode(lay["q"], lay["k_new"], lay["v_new"], lay["k_cache"], lay["v_cache"],
+                                     self.pos, self.W, o=lay["o"], stream=stream)
+            self.pos.add_(1)
 
     def capture(self):
         """Record one decode step into a CUDA graph (after one eager step has run on this device,
