@@ -6,6 +6,7 @@ import torch
 import sliding_window_attention_chunked_b200 as rod
 from sliding_window_attention_chunked_b200 import workloads as wl
 
+from . import row_norms as rn
 from . import sink_ref as ref
 from .test_gpu_sink_paged import DEV, DT, _check_step, _step
 
@@ -150,6 +151,54 @@ def test_extend_bound_of_zero_is_no_bound():
     _check_paged(none, "no tokens", max_len=0)
     args = none.args(DEV)
     assert rod.swska_extend_paged(args[0][:0], *(a[:0] for a in args[1:3]), *args[3:6], args[6][:0], *args[7:], 60, max_len=0).shape == (0, 3, 128)
+
+
+# ---- wide windows, row by row ---------------------------------------------------------------------------------
+WIDE = [("bf16", 128, 5000, 4096, 4), ("bf16", 128, 4800, 4096, 0), ("bf16", 64, 4500, 3000, 5), ("fp32", 64, 4500, 4000, 4), ("fp32", 128, 4300, 4096, 1)]
+
+
+@pytest.mark.parametrize("dtype,d,T,W,S", WIDE)
+def test_training_step_rows_of_a_wide_window(dtype, d, T, W, S):
+    """Flat attention over thousands of keys, each row's error by its norm (row_norms.py): a lost or an extra key shows."""
+    H = 2
+    q, k, v = wl.swska_inputs(1, H, T, d, d, seed=T + d, dtype="fp32", device=DEV)
+    dO = torch.randn(1, H, T, d, device=DEV, generator=torch.Generator(DEV).manual_seed(T))
+    q, k, v, dO = ((0.1 * x if n == "q" else x).to(DT[dtype]) for n, x in (("q", q / q.std()), ("k", k / k.std()), ("v", v), ("dO", dO)))
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    t = torch.arange(T, device=DEV)
+    see, a = ref.visible(t, t, W, S), ref.amp(q, k)
+    dk, dk_tol = 0, 0
+    many = slice(300, None)  # rows that see hundreds of keys; keys that hundreds of queries see are those before T - 300
+    seen = slice(None, T - 300)
+    for h in range(H):
+        want = rn.gradients(*(x.double() for x in (q[0, h], k[0], v[0, h], dO[0, h])), see, d ** -0.5, DT[dtype], a)
+        for name, rows in (("o", many), ("dq", many), ("dv", seen)):
+            bad = rn.off(got[name][0, h][rows], want[name][0][rows], want[name][1][rows])
+            assert not bad.any(), f"{name} head {h}: {int(bad.sum())} rows, first {bad.nonzero()[0].tolist()}"
+        dk, dk_tol = dk + want["dk"][0], dk_tol + want["dk"][1]
+    assert not rn.off(got["dk"][0][seen], dk[seen], dk_tol[seen]).any()
+
+
+@pytest.mark.parametrize("dtype,lens", [("bf16", [1, 1, 1, 1]), ("bf16", [5, 1, 16, 2]), ("bf16", [200, 30, 129, 1]), ("fp32", [1, 20, 3, 70])])
+def test_extend_rows_of_a_wide_window(dtype, lens):
+    """The paged form: every kernel, W 4096, each row's error by its norm."""
+    H, W, S, ps, d = 3, 4096, 4, 64, 128
+    b = ref.Batch(dtype, H, d, d, W, S, ps, [4100, 9000, 4500, 6001], lens, seed=sum(lens))
+    b.q = (0.05 * b.q.float()).to(DT[dtype])  # made with spread 2
+    o, args = _paged(b, max_len=b.max_len)
+    rod.check()
+    kp, vp, a = args[3], args[4], ref.amp(b.q, torch.nan_to_num(b.k_pool))
+    for n, (c, m) in enumerate(zip(b.ctx.tolist(), lens)):
+        pos = torch.arange(c, c + m)
+        j = torch.cat([torch.arange(S), torch.arange(c - W + 1, c + m)])
+        pg = b.table[n, j // ps].long()
+        K, V = kp[pg, j % ps].double(), vp[pg, :, j % ps].double()
+        r0 = int(b.cu[n])
+        for h in range(H):
+            want, tol = rn.forward(args[0][r0:r0 + m, h].double(), K, V[:, h], ref.visible(pos, j, W, S).to(DEV), d ** -0.5, DT[dtype], a)
+            bad = rn.off(o[r0:r0 + m, h], want, tol)
+            assert not bad.any(), f"sequence {n} head {h}: {int(bad.sum())} rows"
 
 
 # ---- a stream given by the caller -----------------------------------------------------------------------------
