@@ -183,6 +183,9 @@ __device__ __forceinline__ uint32_t packed_col(int k) { return (uint32_t)(8 * k 
 // peaks, comes last: its dS already uses D + e, its own share of e included. A CTA with a row that has
 // some p above 1/2 in another tile sweeps its tiles once more with D + e; the error that stays
 // otherwise is 2^-9 of D times the sum of several p k_j, below the rounding of dS.
+// That tile's dS goes to dQ in two bf16 parts, 16 bits in all: the first tokens' keys share the direction that draws the queries,
+// which cancels in dQ since sum_j dS_j = 0, and single roundings of their dS would not (dq was off by 2.6e-3 of its norm in
+// place of 1.8e-3). The second part takes the other 32 columns of each half of the S buffer.
 template <bool SINK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -342,6 +345,11 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int k = 0; k < TILE / 16; ++k)
                 tc::mma_ts_lh_warp(tmem + 256u, tmem + s_col(u) + packed_col(k), k_lo + mnstep(k), d_hi, idesc_g,
                                    (u > u0 || k > 0) ? 1u : 0u);
+            if (SINK && S > 0 && u == u0 + n_it - 1) {
+#pragma unroll
+                for (int k = 0; k < TILE / 16; ++k)
+                    tc::mma_ts_lh_warp(tmem + 256u, tmem + s_col(u) + 32u + packed_col(k), k_lo + mnstep(k), d_hi, idesc_g, 1u);
+            }
             tc::mma_commit_warp(&kempty[u % KSLOT]);
         };
         ok = wait_bar_warp(qfull, 0, abort_flag);
@@ -424,7 +432,7 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // phase 2: dS = P (dP - D), packed over this half's first 32 columns of the S buffer
             if (!wait_bar_warp(pfull, (uint32_t)(u & 1), abort_flag)) { ok = false; break; }
             tc::fence_after_sync();
-            const bool last = SINK && u == n_it - 1;
+            const bool last = SINK && u == n_it - 1, two_parts = SINK && S > 0 && (last || u == 2 * n_it - 1);
             if (last) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -460,6 +468,14 @@ ska_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                 }
                 tc::tmem_st16(tS + 16u * c, pk);
+                if (two_parts) {  // what the rounding left
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 ds = f2mul(p2[16 * c + i], f2sub(raw2(dp, 2 * i), d2));
+                        pk[i] = pack_bf16x2(ds.x - bf16lo(pk[i]), ds.y - bf16hi(pk[i]));
+                    }
+                    tc::tmem_st16(tS + 32u + 16u * c, pk);
+                }
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();

@@ -13,7 +13,9 @@
 // D) is a small difference where a row's attention is peaked, and D from the rounded o is off by about
 // 2^-9 of it. So, as in swska_backward_tc.cu, dq sums e = sum p (dP - D) of its rows in fp32 on the
 // way, visits the first tile (where attention with first tokens peaks) last, with D + e, and sweeps
-// again where some p of another tile is above 1/2; the key side gets D + e.
+// again where some p of another tile is above 1/2; the key side gets D + e. The first tokens' keys share the direction
+// that draws the queries, and sum_j dS_j = 0 makes it cancel in dq, which the roundings of their dS do not: their tiles are
+// multiplied by dS in two bf16 parts (dq was off by 2.8e-3 of its norm in place of 1.7e-3 at d 64, by 3.7e-3 at d 32).
 #pragma once
 
 #include <math.h>
@@ -344,6 +346,13 @@ sink_mma_dq_kernel(const bf16_t* __restrict__ q, const bf16_t* __restrict__ k, c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] *= g[n][e] - D[e / 2];
             mul_tile<DK>(sK, s, acc, lane);
+            if (key0_of(i) < S) {  // and what the rounding left of the first tokens' dS
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] -= __bfloat162float(__float2bfloat16_rn(s[n][e]));
+                mul_tile<DK>(sK, s, acc, lane);
+            }
             __syncthreads();
             fetch(i + 2);
         }

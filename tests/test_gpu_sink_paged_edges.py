@@ -201,6 +201,44 @@ def test_extend_rows_of_a_wide_window(dtype, lens):
             assert not bad.any(), f"sequence {n} head {h}: {int(bad.sum())} rows"
 
 
+# ---- gradients where the first tokens draw attention ------------------------------------------------------------
+@pytest.mark.parametrize("B,H,T,d,W,S", [(2, 2, 1500, 64, 300, 8), (1, 2, 1999, 128, 500, 13), (1, 2, 900, 128, 700, 60), (1, 2, 1200, 64, 90, 128),
+                                         (2, 2, 700, 32, 100, 100), (1, 2, 1000, 128, 200, 128), (1, 3, 127, 128, 40, 20)])
+def test_query_gradients_where_the_first_tokens_draw_attention(B, H, T, d, W, S):
+    """The first tokens' keys share a direction that draws the queries to them. sum_j dS_j = 0, so that direction cancels in dq =
+    sum_j dS_j k_j, and roundings of those dS would be left of it. Held by the norm of the whole dq: its own rounding and those of the dS of
+    the other keys, each at most 2^-8 / sqrt(3) of its term on average (row_norms.py), D from the rounded o for those keys, and 2^-13
+    (the cubic of the exponentials) of the first tokens' terms. Rounding their dS too would be 2.5e-3 to 2.8e-3 of |dq|."""
+    g = torch.Generator(DEV).manual_seed(T + d)
+    rnd = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    u = rnd(d)
+    u /= u.norm()
+    q, k = rnd(B, H, T, d) + 4 * u, rnd(B, T, d)
+    k[:, :S] += 8 * u
+    q, k, v, dO = (x.bfloat16() for x in (q, k, rnd(B, H, T, d), rnd(B, H, T, d)))
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    t = torch.arange(T, device=DEV)
+    see, scale = ref.visible(t, t, W, S), d ** -0.5
+    err = size = terms = first = err_D = 0.0
+    for b in range(B):
+        for h in range(H):
+            Q, K, V, G = (x.double() for x in (q[b, h], k[b], v[b, h], dO[b, h]))
+            o, _, p, _ = ref.attend(Q, K, V, see, scale)
+            D = (G * o).sum(1, keepdim=True)
+            dS = p * (G @ V.T - D) * scale
+            dq, k2 = dS @ K, (K * K).sum(1)
+            err += float(((got["dq"][b, h].double() - dq) ** 2).sum())
+            size += float((dq * dq).sum())
+            terms += float((dS[:, S:] ** 2 @ k2[S:]).sum())
+            first += float((dS[:, :S] ** 2 @ k2[:S]).sum())
+            rest = ((p[:, S:] @ K[S:]) ** 2).sum(1)
+            err_D += float((((G * o) ** 2).sum(1) * rest).sum()) * scale ** 2
+    step = 2.0 ** -8 / 3 ** 0.5
+    tol = step * (size + terms + err_D) ** 0.5 * 1.01 + 2.0 ** -13 * first ** 0.5
+    assert err ** 0.5 <= tol, f"{(err / size) ** 0.5:.2e} of |dq|, allowed {tol / size ** 0.5:.2e}"
+
+
 # ---- a stream given by the caller -----------------------------------------------------------------------------
 def _late(stream, ms=20):
     """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
