@@ -277,7 +277,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf16) {
     ExtendPlan p;
     if (max_len > M) max_len = M;
-    // ctas: what the GPU holds at once
+    // ctas: about what the GPU holds at once (on CUDA cores with d 128 half of them fit: two rounds)
     auto route = [&](int i, int rows, int part_rows, int tile, int groups, int ctas, int min_chunk, int rows_div, int split_cost,
                      int64_t items) {
         ExtendRoute& r = p.r[i];
@@ -297,7 +297,7 @@ ExtendPlan extend_plan(int M, int N, int H, int dk, int dv, int max_len, bool bf
         // Up to four heads a CTA, two CTAs an SM, or up to eight and one: eight fetch a key tile once for
         // all, four put twice the CTAs to work on small batches and leave each less to add up. H 16, W 4096:
         // 17.5 us for 2 sequences with eight, 16.9 with four; 59.5 both for 16; 177 and 183 for 64, 335 and
-        // 346 for 128
+        // 346 for 128 (short runs)
         const int heads = (int64_t)N * ((H + kFewHeads - 1) / kFewHeads) >= 48 ? kFewHeads : kFewHeads / 2;
         const int groups = (H + heads - 1) / heads, hpg = (H + groups - 1) / groups;
         route(0, kFewRows, few, kFewTile, groups, (hpg <= kFewHeads / 2 ? 2 : 1) * sms, 2, 16, 6, N);

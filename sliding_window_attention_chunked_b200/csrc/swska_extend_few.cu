@@ -9,7 +9,8 @@
 // tcgen05 tile of 128 rows would be seven eighths padding), and two warps that feed a ring of
 // stages by TMA. With eight heads a stage (a key tile and eight value tiles) is 72 KB and an SM holds
 // three; with up to four, two CTAs an SM hold two stages of 40 KB each. Both are more than the bytes in
-// flight that HBM's rate times its latency asks of an SM (128 sequences, H 16, W 4096: 335 us, 6.9 TB/s). The pages' rows land in shared
+// flight that HBM's rate times its latency asks of an SM (128 sequences, H 16, W 4096: 330 us and
+// 7.0 TB/s in a short run, 352 to 386 us over seconds of passes). The pages' rows land in shared
 // memory with the 128-byte swizzle, which keeps the fragment loads free of bank conflicts; a page of
 // any multiple of 8 tokens is a row of boxes of 8, 16 or 32 rows. A warp issues a copy every 100
 // clocks or so, and a tile has to come every 3100 at HBM's rate, so a box takes the rows of all of
