@@ -364,7 +364,8 @@ ROD_API int rod_swska_cache_fill_fp8(const void* k, const void* v, void* k_cache
  * outputs dq, dk, dv in the layouts and dtype of q, k, v; workspace of
  * rod_swska_sink_backward_workspace_size bytes (its content on entry is irrelevant). Every sum is
  * taken in a fixed order: the results do not depend on timing. Outputs and workspace overlap no
- * input and not one another.
+ * input and not one another. A NaN or an infinity in a row of v or dO may reach every query and key of the
+ * tiles that the row is part of, in its sequence and head (a probability of 0 times it).
  * Routes: ROD_BF16 with dk = dv = 128 and T >= 128 runs on tcgen05, other ROD_BF16 shapes on
  * warp-level matrix instructions (both: bf16 probabilities and dS, of the first tokens' keys for dq in
  * two bf16 parts; fp32 sums), ROD_FP32 on CUDA cores with fp32 FMAs. A row that sees one key has dS = 0:
@@ -405,7 +406,8 @@ ROD_API int rod_swska_sink_backward(const void* q, const void* k, const void* v,
  * Then query i of sequence n, at position p = ctx[n] + i, attends over the keys j <= p with
  * j > p - window or j < sinks, read from the cache (scale as for rod_swska_prefill). Keys of pages
  * that the table does not have are left out (as pages behind the window are, once given back); a row
- * that sees no key is 0. Memory of a page past its sequence's last token may hold anything. A sequence with ctx[n] < 0 or a
+ * that sees no key is 0. Memory of a page past its sequence's last token may hold anything. (A NaN or an
+ * infinity in a value that some new token sees may reach that sequence's other new tokens.) A sequence with ctx[n] < 0 or a
  * position of 2^31 - 1 or more gets NaN rows. A sequence may have no new token.
  *   max_len: at most this many new tokens per sequence (a bound that picks the kernels; 0: M); of a
  *   longer sequence only the first max_len rows are computed.

@@ -81,6 +81,28 @@ def test_page_tables_keep_all_first_tokens(S, ps):
         assert x == (y if isinstance(y, int) else list(y))
 
 
+@pytest.mark.parametrize("N,M", [(2000, 1700), (16384, 14000)])
+def test_page_tables_of_the_most_sequences(N, M):
+    """A step of thousands of sequences: a few tokens, one, none, finished ones, and fewer tokens than are wanted."""
+    r = torch.Generator().manual_seed(N)
+    rand = lambda hi, *s: torch.randint(0, hi, s, generator=r)
+    ps, W, S, mp = 16, 40, 4, 6
+    ctx = rand(mp * ps - 20, N).tolist()
+    new = [(-1, 0, 1, 1, 1, 3)[x] for x in rand(6, N).tolist()]
+    free = torch.randperm(6 * N, generator=r).tolist()
+    table = [[free.pop() if p * ps < c and (p == 0 or (p + 1) * ps > c - W) else -1 for p in range(mp)] for c in ctx]
+    top = len(free) // 60
+    args = (ctx, new, table, [0] * N, free[:top] + [-1] * (6 * N - top), top, ps, W, S, M)
+    dev = lambda x, dt=torch.int32: torch.tensor(x, dtype=dt, device=DEV)
+    t, f, fl, fc = dev(table), dev([0] * N), dev(args[4]), dev([top])
+    cu, slot = rod.swska_page_tables(dev(ctx, torch.int64), dev(new), t, f, fl, fc, ps, W, S, M)
+    rod.check()
+    want = ref.page_tables(*args)
+    assert 0 < want[4][-1] < sum(max(x, 0) for x in new)
+    for x, y in zip((t.tolist(), f.tolist(), fl.tolist(), int(fc), cu.tolist(), slot.tolist()), want):
+        assert x == (y if isinstance(y, int) else list(y))
+
+
 def test_page_tables_largest_slot_map():
     """A slot map of 2^31 - 1 tokens is filled to its end and no further."""
     M, i32 = 2 ** 31 - 1, lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
@@ -151,6 +173,31 @@ def test_extend_bound_of_zero_is_no_bound():
     _check_paged(none, "no tokens", max_len=0)
     args = none.args(DEV)
     assert rod.swska_extend_paged(args[0][:0], *(a[:0] for a in args[1:3]), *args[3:6], args[6][:0], *args[7:], 60, max_len=0).shape == (0, 3, 128)
+
+
+@pytest.mark.parametrize("dtype,bound", [("bf16", 1), ("bf16", None), ("fp32", 1)])
+def test_extend_the_most_sequences(dtype, bound):
+    """16384 sequences of one token, each in a page of its own; every third one idle."""
+    N, H, d, ps = 16384, 2, 128, 8
+    g = torch.Generator(DEV).manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, device=DEV, generator=g).to(DT[dtype])
+    n = torch.arange(N, device=DEV)
+    ctx, lens = (n * 5) % ps, (n % 3 != 2).to(torch.int32)
+    table = torch.randperm(N, device=DEV, generator=g).to(torch.int32)[:, None]
+    cu = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).to(torch.int32)
+    who = n[lens == 1]
+    M, page = len(who), table[who, 0]
+    slot = page * ps + ctx[who].to(torch.int32)
+    kp, vp, q, kn, vn = rnd(N, ps, d), rnd(N, H, ps, d), rnd(M, H, d), rnd(M, d), rnd(M, H, d)
+    o = rod.swska_extend_paged(q, kn, vn, kp, vp, table, slot, cu, ctx, 5, sinks=1, max_len=bound)
+    rod.check()
+    assert torch.equal(kp[page.long(), ctx[who]], kn) and torch.equal(vp[page.long(), :, ctx[who]], vn)
+    j = torch.arange(ps, device=DEV)
+    see = (j <= ctx[who, None]) & ((j > ctx[who, None] - 5) | (j < 1))
+    K, V = kp[page.long()].double(), vp[page.long()].double()
+    s = torch.where(see[:, None], torch.einsum("mhd,mjd->mhj", q.double(), K) * d ** -0.5, -torch.inf)
+    p = torch.softmax(s, -1)
+    ref.check(o, torch.einsum("mhj,mhjd->mhd", p, V), torch.einsum("mhj,mhjd->mhd", p, V.abs()), 6, d, ref.amp(q, kp), f"most {dtype}")
 
 
 # ---- wide windows, row by row ---------------------------------------------------------------------------------
