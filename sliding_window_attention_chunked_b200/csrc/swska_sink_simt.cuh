@@ -69,9 +69,9 @@ template <int DK, int DV> struct Dq {
     static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP;
     static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
 };
-// dk, dv: K, V | per group Q, dO, P, log-sum-exp, D
+// dk, dv: K, V | per group Q, dO, P, log-sum-exp, D, e
 template <int DK, int DV> struct Dkv {
-    static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP + 2 * BK;
+    static constexpr int own = BQ * (ld<DK>() + ld<DV>()), each = BK * (ld<DK>() + ld<DV>()) + BQ * LDP + 3 * BK;
     static constexpr int NG = groups_for(own, each), smem = (own + NG * each) * 4;
     static_assert(2 * BK == NTH, "a thread of the group per log-sum-exp and D of a tile");
 };
@@ -209,7 +209,8 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dq<DK, DV>::NG)
 sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ dO,
-               float* __restrict__ dq, float* __restrict__ dbuf, int H, int T, int W, int S, float scale, int qtiles) {
+               float* __restrict__ dq, float* __restrict__ dbuf, float* __restrict__ ebuf, int H, int T, int W, int S, float scale,
+               int qtiles) {
     constexpr int NG = Dq<DK, DV>::NG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the key side may set itself up
     extern __shared__ __align__(16) float sm[];
@@ -240,6 +241,9 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
     // attention, o is that key's v and dP - D is exactly 0, not the difference of two roundings (shared out over
     // 16 threads a row, dq and dk of rows that see one key were 1e-7 |dO| |v| of noise). The rows of o wait in the dS
     // tiles, 64 columns to a group's.
+    // Where all keys of the CTA's rows lie in one tile, what D is off by, e = sum_j p_j (dP_j - D), is taken out too (sum_j dS_j = 0):
+    // dS = p ((dP - D) - e), whose terms are small where attention is peaked (dq of two tokens, the first drawing attention, was
+    // off by up to 1e-3 of its norm). With more tiles dq would need a second sweep, for rows that such peaks are few of.
     static_assert(DV <= BK || NG >= 2, "room for the rows of o");
     float* sO = sm + Dq<DK, DV>::own + BK * (ld<DK>() + ld<DV>());
     auto o_at = [&](int r, int c) { return sO + (c / BK) * Dq<DK, DV>::each + r * LDP + c % BK; };
@@ -268,7 +272,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
         if (t0 + r < T) dbuf[bh * T + t0 + r] = sum.x + sum.y;
     }
     __syncthreads();
-    float L2[4], D[4], acc[4][DK / 16];
+    float L2[4], D[4], e[4] = {0.f, 0.f, 0.f, 0.f}, acc[4][DK / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i, t = t0 + r;
@@ -292,8 +296,21 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool see = ska_visible(t0 + 4 * ty + i, key0 + tx + 16 * j, W, S);
-                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) * (g[i][j] - D[i]) : 0.f;
+                g[i][j] -= D[i];
+                s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -L2[i])) : 0.f;
             }
+        if (kt.n == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[i] = fmaf(s[i][j], g[i][j], e[i]);
+                e[i] = row_sum(e[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] *= g[i][j] - e[i];
         put_tile(sP, ty, tx, s);
         group_sync<NTH>(g0);
         tile_mul<DK>(sP, sK, ty, tx, acc);
@@ -316,6 +333,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + 4 * ty + i;
         if (t >= T) continue;
+        if (tx == 0) ebuf[bh * T + t] = e[i];
 #pragma unroll
         for (int c = 0; c < DK / 16; ++c)
             dq[(bh * T + t) * (int64_t)DK + Cols<DK>::at(tx, c)] = acc[i][c] * scale;
@@ -326,7 +344,7 @@ sink_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const f
 template <int DK, int DV>
 __global__ void __launch_bounds__(NTH * Dkv<DK, DV>::NG)
 sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                const float* __restrict__ lse, const float* dbuf, const float* __restrict__ dO,
+                const float* __restrict__ lse, const float* dbuf, const float* ebuf, const float* __restrict__ dO,
                 float* __restrict__ dv, SinkParts parts, int B, int H, int T, int W, int S, float scale) {
     constexpr int NG = Dkv<DK, DV>::NG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that adds the parts waits for the end
@@ -340,6 +358,7 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     float* sP = sG + BK * ld<DV>();
     float* sL = sP + BQ * LDP;
     float* sD = sL + BK;
+    float* sE = sD + BK;
     const int tiles = parts.ctas();
     const int64_t bh = blockIdx.x / tiles;
     const int b = (int)bh / H, h = (int)bh - b * H;
@@ -360,6 +379,10 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared((tid < BK ? sL : sD) + x)),
                          "l"(from), "r"(t0 + x < T ? 4 : 0)
                          : "memory");
+            if (tid < BK)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(sE + x)),
+                             "l"(ebuf + (t0 + x < T ? bh * T + t0 + x : 0)), "r"(t0 + x < T ? 4 : 0)
+                             : "memory");
         }
         copies_sent();
     };
@@ -395,7 +418,7 @@ sink_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
                 const int c = tx + 16 * j;
                 const bool see = t0 + c < T && ska_visible(t0 + c, key0 + 4 * ty + i, W, S);
                 s[i][j] = see ? exp2f(fmaf(s[i][j], scale_log2, -kLog2e * sL[c])) : 0.f;
-                g[i][j] = s[i][j] * (g[i][j] - sD[c]);
+                g[i][j] = s[i][j] * ((g[i][j] - sD[c]) - sE[c]);
             }
         put_tile(sP, ty, tx, s);
         group_sync<NTH>(g0);
@@ -465,6 +488,7 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     const int qtiles = (a.T + BQ - 1) / BQ;
     SinkParts parts = sink_parts_plan(a, BQ, BK, a.H);
     float* dbuf = sink_parts_bind(parts, a);
+    float* ebuf = dbuf + (size_t)a.B * a.H * a.T;  // the second array of row statistics
     const int64_t grid = (int64_t)qtiles * a.B * a.H, key_grid = (int64_t)parts.ctas() * a.B * a.H;
     if (grid > 0x7fffffffLL || key_grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e;
@@ -472,10 +496,11 @@ cudaError_t bwd_t(const SinkArgs& a, cudaStream_t s) {
     if ((e = allow_smem(q_set, (const void*)sink_dq_kernel<DK, DV>, Q::smem)) != cudaSuccess) return e;
     if ((e = allow_smem(k_set, (const void*)sink_dkv_kernel<DK, DV>, K::smem)) != cudaSuccess) return e;
     sink_dq_kernel<DK, DV><<<(unsigned)grid, NTH * Q::NG, Q::smem, s>>>(
-        f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
+        f32(a.q), f32(a.k), f32(a.v), f32(a.o), a.lse, f32(a.dO), static_cast<float*>(a.dq), dbuf, ebuf, a.H, a.T, a.W, a.S, a.scale, qtiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_overlapped(sink_dkv_kernel<DK, DV>, dim3((unsigned)key_grid), dim3(NTH * K::NG),
-                          K::smem, s, f32(a.q), f32(a.k), f32(a.v), a.lse, static_cast<const float*>(dbuf), f32(a.dO),
+                          K::smem, s, f32(a.q), f32(a.k), f32(a.v), a.lse, static_cast<const float*>(dbuf),
+                          static_cast<const float*>(ebuf), f32(a.dO),
                           static_cast<float*>(a.dv), parts, a.B, a.H, a.T, a.W, a.S, a.scale);
     note_launches(2);
     if (e != cudaSuccess) return e;

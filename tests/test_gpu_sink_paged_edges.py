@@ -286,6 +286,45 @@ def test_query_gradients_where_the_first_tokens_draw_attention(B, H, T, d, W, S)
     assert err ** 0.5 <= tol, f"{(err / size) ** 0.5:.2e} of |dq|, allowed {tol / size ** 0.5:.2e}"
 
 
+@pytest.mark.parametrize("T,dk,dv,W,S", [(2, 16, 16, 36, 1), (2, 32, 128, 1, 1), (5, 16, 16, 153, 1), (33, 64, 64, 40, 2), (64, 128, 128, 64, 1), (60, 32, 64, 9, 0)])
+def test_fp32_gradients_where_attention_is_peaked_in_one_tile(T, dk, dv, W, S):
+    """fp32 rows whose keys lie in one key tile and that give one of them nearly everything: dS = p (dP - D) is a small difference of
+    large sums. An error of D is taken out (sum_j dS_j = 0 as computed), which leaves, with A_j = |dO| . |v_j| and u = 2^-23 for 32 bits:
+    the relative errors of p and dP - D, and those of the dP_j, d u A_j, which enter dS_j as p_j (err_j - sum_k p_k err_k) and so only with
+    the weights of the others, (1 - p_j) A_j + sum_{k != j} p_k A_k; the sum e of the differences, rounded to 4 u of its terms; and the
+    roundings of dP and D in the 64-bit reference, dv 2^-52 of A_j and of sum_k p_k A_k (a row that sees one key has nothing else)."""
+    B, H = 2, 3
+    q, k, v = wl.swska_inputs(B, H, T, dk, dv, seed=T + dk, dtype="fp32", device=DEV)
+    g = torch.Generator(DEV).manual_seed(T)
+    dO, w = torch.randn(B, H, T, dv, device=DEV, generator=g), torch.randn(dk, device=DEV, generator=g)
+    w /= w.norm()
+    q = q + dk ** 0.5 * w
+    k[:, ::max(W, 2) if S == 0 else T] += 11 * w
+    got = _step(q, k, v, dO, W, S)
+    rod.check()
+    t = torch.arange(T, device=DEV)
+    see, scale, u = ref.visible(t, t, W, S), dk ** -0.5, 2.0 ** -23
+    inner = (T + dk + dv) * u * (1 + ref.amp(q, k)) + 2.0 ** -20
+    dk_want, dk_tol, peaked = torch.zeros_like(k, dtype=torch.float64), torch.zeros_like(k, dtype=torch.float64), 0
+    for b in range(B):
+        for h in range(H):
+            Q, K, V, G = (x.double() for x in (q[b, h], k[b], v[b, h], dO[b, h]))
+            o, _, p, _ = ref.attend(Q, K, V, see, scale)
+            dP = G @ V.T - (G * o).sum(1, keepdim=True)
+            A, a = G.abs() @ V.abs().T, (p * dP.abs()).sum(1, keepdim=True)
+            err = inner * p * (dP.abs() + a) + dv * u * p * ((1 - p) * A + (p * A).sum(1, keepdim=True) - p * A) + 4 * u * p * a
+            err = err + dv * 2.0 ** -52 * p * (A + (p * A).sum(1, keepdim=True))
+            want, tol = (p * dP) @ K * scale, err @ K.abs() * scale
+            bad = (got["dq"][b, h].double() - want).abs() > tol + u * want.abs() + 1e-30
+            assert not bad.any(), f"dq {b} {h}: {int(bad.sum())} off at {bad.nonzero()[0].tolist()}"
+            dk_want[b] += (p * dP).T @ Q * scale
+            dk_tol[b] += err.T @ Q.abs() * scale
+            peaked += int(((p.max(1).values > 0.99) & (see.sum(1) > 1)).sum())
+    bad = (got["dk"].double() - dk_want).abs() > dk_tol + H * u * dk_want.abs() + 1e-30
+    assert not bad.any(), f"dk: {int(bad.sum())} off at {bad.nonzero()[0].tolist()}"
+    assert peaked > 0
+
+
 # ---- a stream given by the caller -----------------------------------------------------------------------------
 def _late(stream, ms=20):
     """Work that keeps a stream busy for some milliseconds, so that a call on it has not begun when it returns."""
